@@ -1,0 +1,37 @@
+// Matrices held in 8-bit floating point with one scale per block of 128:
+// internal declarations of the quantiser, the products and the rank-r gradient.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "internal.cuh"
+#include "kernels.cuh"
+
+namespace qlora {
+
+// Scale blocks along one axis of `n` elements.
+inline int64_t f8_blocks(int64_t n) { return ceil_div(n, 128); }
+
+// abi_f8.cu: shape and pointer checks of a qlora_f8.
+qlora_status check_f8(const qlora_f8& q);
+
+// f8_quantize.cu
+qlora_status launch_f8_quantize(const void* X, int32_t x_dtype, const qlora_f8& q, cudaStream_t s);
+qlora_status launch_f8_dequantize(const qlora_f8& q, void* out, int32_t out_dtype,
+                                  cudaStream_t s);
+
+// The LoRA term of a product, added as extra stages of the same accumulators:
+// C += hi . R + lo . R with [hi | lo] = L (m x 2 lora_span(r) bf16) and R (bf16)
+// B (n x r, K-major) in the forward, A (r x n, MN-major) in the backward.
+struct F8Lora {
+  const void* L;
+  const void* R;
+  int32_t r;  // 0 = no LoRA term
+};
+
+// f8_gemm.cu: C (m x n, row-major, bf16 or fp32) = A . B^T (trans_b) or A . B,
+// A by rows, B by tiles, plus the LoRA term.  Any sizes; m >= 1.
+qlora_status f8_gemm(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,
+                     const F8Lora& lora, cudaStream_t s);
+
+}  // namespace qlora

@@ -7,6 +7,7 @@ in the library's CUDA kernels.  A missing library raises immediately: there
 is no other implementation to fall back to.
 """
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -30,6 +31,11 @@ QLORA_F32 = 0
 QLORA_BF16 = 1
 QLORA_TABLE_NF4 = 0
 QLORA_TABLE_UNIFORM = 1
+
+QLORA_E4M3 = 0
+QLORA_E5M2 = 1
+QLORA_F8_ROWS = 0
+QLORA_F8_TILES = 1
 
 QLORA_KERNEL_QUANTIZE = 0
 QLORA_KERNEL_FUSED_FWD = 1
@@ -59,6 +65,14 @@ class qlora_adapter_opts(ctypes.Structure):
     ]
 
 
+class qlora_f8(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ld", ctypes.c_int64),
+        ("layout", ctypes.c_int32), ("format", ctypes.c_int32), ("pow2", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+    ]
+
+
 class QloraError(RuntimeError):
     def __init__(self, status, where):
         self.status = int(status)
@@ -81,6 +95,7 @@ def lib():
         psz = ctypes.POINTER(ctypes.c_size_t)
         pq = ctypes.POINTER(qlora_nf4)
         po = ctypes.POINTER(qlora_adapter_opts)
+        pf = ctypes.POINTER(qlora_f8)
         sig = {
             "qlora_status_string": (ctypes.c_char_p, [ctypes.c_int]),
             "qlora_levels": (ctypes.c_int, [i32, ctypes.POINTER(ctypes.c_float)]),
@@ -99,6 +114,10 @@ def lib():
                                                    sz, vp]),
             "qlora_linear_bwd_ex": (ctypes.c_int, [pq, vp, vp, i32, f32, po, vp, vp, vp, i64, vp,
                                                    vp, vp, i32, vp, sz, vp]),
+            "qlora_f8_sizes": (ctypes.c_int, [i64, i64, i32, ctypes.POINTER(i64), psz, psz]),
+            "qlora_f8_quantize": (ctypes.c_int, [vp, i32, pf, vp]),
+            "qlora_f8_dequantize": (ctypes.c_int, [pf, vp, i32, vp]),
+            "qlora_f8_matmul": (ctypes.c_int, [pf, pf, i32, vp, i32, vp]),
             "qlora_check": (ctypes.c_int, [vp, vp]),
             "qlora_selftest_timeout": (ctypes.c_int, [i64, vp, vp]),
             "qlora_merge": (ctypes.c_int, [pq, vp, vp, i32, f32, vp, vp]),
@@ -473,6 +492,133 @@ def qlora_adamw(param, grad, m, v, step, lr, beta1=0.9, beta2=0.999, eps=1e-8,
     _ok(lib().qlora_adamw(_ptr(param), _ptr(param_bf16), _ptr(grad), _ptr(m), _ptr(v), n,
                           int(step), float(lr), float(beta1), float(beta2), float(eps),
                           float(weight_decay), float(grad_scale), _stream(stream)), "qlora_adamw")
+
+
+_F8_DTYPE = {QLORA_E4M3: torch.float8_e4m3fn, QLORA_E5M2: torch.float8_e5m2}
+
+
+def qlora_f8_sizes(rows, cols, layout=QLORA_F8_ROWS):
+    ld, codes, scales = ctypes.c_int64(), ctypes.c_size_t(), ctypes.c_size_t()
+    _ok(lib().qlora_f8_sizes(rows, cols, layout, ctypes.byref(ld), ctypes.byref(codes),
+                             ctypes.byref(scales)), "qlora_f8_sizes")
+    return {"ld": ld.value, "codes": codes.value, "scales": scales.value}
+
+
+def _f8_scales_shape(rows, cols, layout):
+    kb = -(-cols // 128)
+    return (kb, rows) if layout == QLORA_F8_ROWS else (-(-rows // 128), kb)
+
+
+class F8Matrix:
+    """Caller-owned device arrays of a matrix held in 8 bits (see qlora_f8): codes (uint8,
+    rows x ld) and scales (fp32: blocks x rows, or row blocks x column blocks for tiles)."""
+
+    def __init__(self, rows, cols, layout, format, pow2, codes, scales):
+        if layout not in (QLORA_F8_ROWS, QLORA_F8_TILES) or format not in _F8_DTYPE:
+            raise ValueError(f"layout {layout}, format {format}: expected QLORA_F8_ROWS or "
+                             "QLORA_F8_TILES, and QLORA_E4M3 or QLORA_E5M2")
+        shape = _f8_scales_shape(rows, cols, layout)
+        if (codes.dtype != torch.uint8 or codes.dim() != 2 or codes.shape[0] != rows
+                or codes.shape[1] < cols or codes.shape[1] % 16 or not codes.is_contiguous()):
+            raise ValueError(f"codes: expected a contiguous uint8 tensor of {rows} rows of at least "
+                             f"{cols} bytes, a multiple of 16, got {codes.dtype} "
+                             f"{tuple(codes.shape)}")
+        if (scales.dtype != torch.float32 or tuple(scales.shape) != shape
+                or not scales.is_contiguous() or scales.device != codes.device):
+            raise ValueError(f"scales: expected a contiguous fp32 tensor of shape {shape} beside "
+                             f"the codes, got {scales.dtype} {tuple(scales.shape)} on "
+                             f"{scales.device}")
+        self.rows, self.cols, self.layout, self.format = rows, cols, layout, format
+        self.pow2, self.codes, self.scales = bool(pow2), codes, scales
+        self.struct = qlora_f8(rows, cols, codes.shape[1], layout, format, int(self.pow2), 0,
+                               codes.data_ptr(), scales.data_ptr())
+
+    @classmethod
+    def empty(cls, rows, cols, layout=QLORA_F8_ROWS, format=QLORA_E4M3, pow2=False,
+              device="cuda"):
+        if rows < 0 or cols < 1:
+            raise ValueError(f"a matrix of {rows} x {cols}")
+        return cls(rows, cols, layout, format, pow2,
+                   torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device),
+                   torch.empty(_f8_scales_shape(rows, cols, layout), dtype=torch.float32,
+                               device=device))
+
+    @property
+    def values(self):
+        """The codes as 8-bit floating point numbers (rows x cols, without the scales)."""
+        v = self.codes.view(_F8_DTYPE[self.format])
+        return v if v.shape[1] == self.cols else v[:, :self.cols]
+
+    @property
+    def nbytes(self):
+        return self.codes.numel() + 4 * self.scales.numel()
+
+
+def _on_current_device(*tensors):
+    """The library launches on the current device: refuse tensors that live elsewhere."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
+def _in_stream(stream):
+    """Allocate for work on `stream`: memory taken here is reused in that stream's order."""
+    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def qlora_f8_quantize(X, layout=QLORA_F8_ROWS, format=QLORA_E4M3, pow2=False, out=None,
+                      stream=None):
+    """Quantise a 2-D fp32/bf16 CUDA tensor in blocks of 128; returns an F8Matrix.  With `out`
+    its layout, format and pow2 are taken."""
+    if not X.is_cuda or X.dim() != 2 or not X.is_contiguous() or X.dtype not in _DTYPE:
+        raise ValueError(f"X: expected a contiguous 2-D fp32 or bf16 CUDA tensor, got {X.dtype} "
+                         f"{tuple(X.shape)} on {X.device}")
+    rows, cols = X.shape
+    if out is None:
+        with _in_stream(stream):
+            out = F8Matrix.empty(rows, cols, layout, format, pow2, X.device)
+    elif (out.rows, out.cols) != (rows, cols):
+        raise ValueError(f"out holds a {out.rows} x {out.cols} matrix, X is {rows} x {cols}")
+    _on_current_device(X, out.codes)
+    _ok(lib().qlora_f8_quantize(X.data_ptr(), _DTYPE[X.dtype], out.struct, _stream(stream)),
+        "qlora_f8_quantize")
+    return out
+
+
+def _f8_out(out, shape, dtype, device, stream, name):
+    if out is None:
+        if dtype not in _DTYPE:
+            raise ValueError(f"{name}: fp32 or bf16, not {dtype}")
+        with _in_stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    if (tuple(out.shape) != shape or out.dtype not in _DTYPE or not out.is_contiguous()
+            or out.device != device):
+        raise ValueError(f"{name}: expected a contiguous fp32 or bf16 tensor of shape {shape} on "
+                         f"{device}, got {out.dtype} {tuple(out.shape)} on {out.device}")
+    return out
+
+
+def qlora_f8_dequantize(q, dtype=torch.bfloat16, out=None, stream=None):
+    """The values of an F8Matrix, code times scale, as a bf16 or fp32 tensor."""
+    out = _f8_out(out, (q.rows, q.cols), dtype, q.codes.device, stream, "out")
+    _on_current_device(q.codes)
+    _ok(lib().qlora_f8_dequantize(q.struct, out.data_ptr(), _DTYPE[out.dtype], _stream(stream)),
+        "qlora_f8_dequantize")
+    return out
+
+
+def qlora_f8_matmul(a, b, trans_b=True, dtype=torch.bfloat16, out=None, stream=None):
+    """a b^T (trans_b: b is n x k) or a b (b is k x n) of two F8Matrix, a by rows, b by tiles."""
+    k, n = (b.cols, b.rows) if trans_b else (b.rows, b.cols)
+    if a.cols != k:
+        raise ValueError(f"a is {a.rows} x {a.cols}, b is {b.rows} x {b.cols} "
+                         f"({'transposed' if trans_b else 'not transposed'})")
+    out = _f8_out(out, (a.rows, n), dtype, a.codes.device, stream, "out")
+    _on_current_device(a.codes, b.codes)
+    _ok(lib().qlora_f8_matmul(a.struct, b.struct, 1 if trans_b else 0, out.data_ptr(),
+                              _DTYPE[out.dtype], _stream(stream)), "qlora_f8_matmul")
+    return out
 
 
 class _PagedBlock:

@@ -295,6 +295,67 @@ qlora_status qlora_linear_bwd_ex(const qlora_nf4* W, const void* A, const void* 
                                  float* dB, int32_t accumulate, void* workspace,
                                  size_t workspace_bytes, void* stream);
 
+/* Matrices held in 8-bit floating point with one scale per block of 128: kept
+ * activations, gradients, and merged or 8-bit base weights.
+ *   layout  QLORA_F8_ROWS: a scale per row and 128 consecutive columns, stored
+ *           block column by block column: scales[kb * rows + row], kb = col / 128
+ *           (activations and gradients, left operands);
+ *           QLORA_F8_TILES: a scale per 128 x 128 tile, row-major:
+ *           scales[(row / 128) * ceil(cols / 128) + col / 128] (weights)
+ *   format  QLORA_E4M3 (largest value F = 448) or QLORA_E5M2 (F = 57344)
+ *   pow2    1: the scales are powers of two, 0: any fp32
+ *   codes   device, rows of ld bytes (ld a multiple of 16, at least cols)
+ *   scales  device fp32
+ * The value of an element is its code times its block's scale.  Sizes need not
+ * be multiples of 128: the last blocks are smaller.  rows = 0 is allowed. */
+typedef enum { QLORA_E4M3 = 0, QLORA_E5M2 = 1 } qlora_f8_format;
+typedef enum { QLORA_F8_ROWS = 0, QLORA_F8_TILES = 1 } qlora_f8_layout;
+typedef struct {
+  int64_t rows, cols;
+  int64_t ld;
+  int32_t layout;   /* qlora_f8_layout */
+  int32_t format;   /* qlora_f8_format */
+  int32_t pow2;     /* 0 or 1 */
+  int32_t reserved; /* set to 0 */
+  uint8_t* codes;
+  float* scales;
+} qlora_f8;
+
+/* The smallest ld and the byte sizes of the arrays of a rows x cols matrix (any
+ * output may be NULL).  QLORA_ERR_SHAPE for rows < 0, cols < 1, a side of 2^31 or
+ * more, or more than 2^36 elements; QLORA_ERR_UNSUPPORTED for another layout. */
+qlora_status qlora_f8_sizes(int64_t rows, int64_t cols, int32_t layout, int64_t* ld,
+                            size_t* codes_bytes, size_t* scales_bytes);
+
+/* Quantise X (device, rows x cols values of x_dtype, row-major) into the arrays of
+ * *q.  Per block, with a = max |x| over its finite values:
+ *   s = max(fp32(a / F), 2^-126), or with pow2 the smallest power of two that is at
+ *       least 2^-126 and a / F,
+ *   code = the nearest 8-bit value (ties to even) to fp32(x * fp32(1 / s)).
+ * NaN and infinite values get the format's NaN and leave the others of their block
+ * as they are, so that a bad value shows where it is used.  The bytes of a row past
+ * cols up to the next multiple of 16 are written as zeros.  Needs no workspace.
+ * Errors: QLORA_ERR_NULL, _ALIGN, _SHAPE, _UNSUPPORTED, _CUDA. */
+qlora_status qlora_f8_quantize(const void* X, int32_t x_dtype, const qlora_f8* q, void* stream);
+
+/* Restore *q into X_out (device, rows x cols values of out_dtype, row-major):
+ * fp32 out is fp32(code * s), bf16 out that value rounded to nearest even (exact
+ * with pow2 while in range).  Needs no workspace.  Errors as qlora_f8_quantize. */
+qlora_status qlora_f8_dequantize(const qlora_f8* q, void* X_out, int32_t out_dtype, void* stream);
+
+/* C = A B^T (trans_b != 0: B is n x k) or C = A B (B is k x n) of two such matrices,
+ * A (m x k) with layout QLORA_F8_ROWS, B with QLORA_F8_TILES, each of either format.
+ * C (device, m x n, row-major) is bf16 or fp32, rounded once from fp32 sums:
+ *   C[i][j] = sum over 128-blocks b of k of
+ *             sA[b][i] sB[b, j / 128] (sum over the block of codeA codeB).
+ * The products sA sB have to be finite.  Needs no workspace; the tensor cores'
+ * device-side waits are bounded, and as the call takes no status word, a wait that
+ * gives up (it does not in correct operation) leaves NaN in its tile of C.
+ * Errors: QLORA_ERR_NULL, _ALIGN, _SHAPE (contraction lengths differ, B without
+ * rows, more than 2^36 outputs), _UNSUPPORTED (layouts, types), _CUDA. */
+qlora_status qlora_f8_matmul(const qlora_f8* A, const qlora_f8* B, int32_t trans_b, void* C,
+                             int32_t c_dtype, void* stream);
+
 /* Paged optimiser states.  The optimiser moments can live in CUDA managed
  * (unified) memory, which the driver migrates between host and device pages
  * on demand, so that they need not stay in HBM ("LoRA 与 QLoRA：把大模型微调

@@ -1,0 +1,115 @@
+"""Host-side checks of the 8-bit operators: sizes, refusals before any launch (no GPU needed),
+and the reference's own rounding against torch's 8-bit types."""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import f8_ref as R
+from bit_nf4_quantized_17_b200 import qlora as Q
+
+BUF = 4096  # a fake, aligned device address: these calls return before they use it
+
+
+def _m(rows=64, cols=256, layout=Q.QLORA_F8_ROWS, format=Q.QLORA_E4M3, ld=None, pow2=0,
+       codes=BUF, scales=BUF):
+    return Q.qlora_f8(rows, cols, cols if ld is None else ld, layout, format, pow2, 0, codes,
+                      scales)
+
+
+def test_sizes():
+    assert Q.qlora_f8_sizes(5, 130, Q.QLORA_F8_ROWS) == {"ld": 144, "codes": 720, "scales": 40}
+    assert Q.qlora_f8_sizes(129, 256, Q.QLORA_F8_TILES) == {"ld": 256, "codes": 33024,
+                                                            "scales": 16}
+    assert Q.qlora_f8_sizes(0, 1, Q.QLORA_F8_ROWS) == {"ld": 16, "codes": 0, "scales": 0}
+    for rows, cols, layout, st in ((-1, 8, 0, Q.QLORA_ERR_SHAPE), (8, 0, 0, Q.QLORA_ERR_SHAPE),
+                                   (1 << 31, 1, 0, Q.QLORA_ERR_SHAPE),
+                                   (1 << 20, 1 << 20, 0, Q.QLORA_ERR_SHAPE),
+                                   (8, 8, 2, Q.QLORA_ERR_UNSUPPORTED)):
+        with pytest.raises(Q.QloraError) as e:
+            Q.qlora_f8_sizes(rows, cols, layout)
+        assert e.value.status == st
+
+
+BAD = [
+    (dict(cols=0), Q.QLORA_ERR_SHAPE), (dict(rows=-1), Q.QLORA_ERR_SHAPE),
+    (dict(ld=255), Q.QLORA_ERR_SHAPE), (dict(ld=248), Q.QLORA_ERR_SHAPE),
+    (dict(ld=264), Q.QLORA_ERR_SHAPE), (dict(layout=2), Q.QLORA_ERR_UNSUPPORTED),
+    (dict(format=2), Q.QLORA_ERR_UNSUPPORTED), (dict(pow2=2), Q.QLORA_ERR_UNSUPPORTED),
+    (dict(codes=None), Q.QLORA_ERR_NULL), (dict(scales=None), Q.QLORA_ERR_NULL),
+    (dict(codes=BUF + 8), Q.QLORA_ERR_ALIGN), (dict(scales=BUF + 4), Q.QLORA_ERR_ALIGN),
+]
+
+
+@pytest.mark.parametrize("kw,status", BAD)
+def test_matrix_refused_everywhere(kw, status):
+    L, bad, good = Q.lib(), _m(**kw), _m()
+    tiles = _m(layout=Q.QLORA_F8_TILES)
+    assert L.qlora_f8_quantize(BUF, 0, bad, None) == status
+    assert L.qlora_f8_dequantize(bad, BUF, 0, None) == status
+    assert L.qlora_f8_matmul(bad, tiles, 1, BUF, 0, None) == status
+    assert L.qlora_f8_matmul(good, _m(**{"layout": Q.QLORA_F8_TILES, **kw}), 1, BUF, 0,
+                             None) == status
+
+
+def test_call_refusals():
+    L, a = Q.lib(), _m()
+    b = _m(layout=Q.QLORA_F8_TILES)
+    null = ctypes.POINTER(Q.qlora_f8)()
+    assert L.qlora_f8_quantize(BUF, 0, null, None) == Q.QLORA_ERR_NULL
+    assert L.qlora_f8_quantize(None, 0, a, None) == Q.QLORA_ERR_NULL
+    assert L.qlora_f8_quantize(BUF + 2, 1, a, None) == Q.QLORA_ERR_ALIGN
+    assert L.qlora_f8_quantize(BUF, 2, a, None) == Q.QLORA_ERR_UNSUPPORTED
+    assert L.qlora_f8_dequantize(a, None, 0, None) == Q.QLORA_ERR_NULL
+    assert L.qlora_f8_dequantize(a, BUF, 5, None) == Q.QLORA_ERR_UNSUPPORTED
+    assert L.qlora_f8_dequantize(a, BUF + 4, 0, None) == Q.QLORA_ERR_ALIGN
+    assert L.qlora_f8_matmul(null, b, 1, BUF, 0, None) == Q.QLORA_ERR_NULL
+    assert L.qlora_f8_matmul(a, null, 1, BUF, 0, None) == Q.QLORA_ERR_NULL
+    assert L.qlora_f8_matmul(a, b, 1, None, 0, None) == Q.QLORA_ERR_NULL
+    assert L.qlora_f8_matmul(a, b, 1, BUF + 8, 0, None) == Q.QLORA_ERR_ALIGN
+    assert L.qlora_f8_matmul(a, b, 1, BUF, 7, None) == Q.QLORA_ERR_UNSUPPORTED
+    assert L.qlora_f8_matmul(a, a, 1, BUF, 0, None) == Q.QLORA_ERR_UNSUPPORTED
+    assert L.qlora_f8_matmul(b, b, 1, BUF, 0, None) == Q.QLORA_ERR_UNSUPPORTED
+    # contraction lengths: A is 64 x 256, B 64 x 256
+    assert L.qlora_f8_matmul(a, b, 0, BUF, 0, None) == Q.QLORA_ERR_SHAPE
+    assert L.qlora_f8_matmul(a, _m(cols=272, layout=Q.QLORA_F8_TILES), 1, BUF, 0,
+                             None) == Q.QLORA_ERR_SHAPE
+    assert L.qlora_f8_matmul(a, _m(rows=0, layout=Q.QLORA_F8_TILES), 1, BUF, 0,
+                             None) == Q.QLORA_ERR_SHAPE
+    # no rows: nothing to do, nothing asked of the pointers
+    empty = _m(rows=0, codes=None, scales=None)
+    assert L.qlora_f8_quantize(None, 0, empty, None) == Q.QLORA_OK
+    assert L.qlora_f8_dequantize(empty, None, 0, None) == Q.QLORA_OK
+    assert L.qlora_f8_matmul(empty, b, 1, None, 0, None) == Q.QLORA_OK
+
+
+def test_binding_refusals():
+    u8 = torch.uint8
+    good = dict(rows=4, cols=130, layout=Q.QLORA_F8_ROWS, format=Q.QLORA_E4M3, pow2=False,
+                codes=torch.zeros(4, 144, dtype=u8), scales=torch.zeros(2, 4))
+    q = Q.F8Matrix(**good)
+    assert q.values.shape == (4, 130) and q.nbytes == 4 * 144 + 32
+    for kw in (dict(codes=torch.zeros(4, 136, dtype=u8)), dict(codes=torch.zeros(4, 128, dtype=u8)),
+               dict(codes=torch.zeros(4, 144)), dict(scales=torch.zeros(4, 2)),
+               dict(scales=torch.zeros(2, 4, dtype=torch.float64)), dict(layout=5), dict(format=9),
+               dict(codes=torch.zeros(4, 288, dtype=u8)[:, ::2])):
+        with pytest.raises(ValueError):
+            Q.F8Matrix(**{**good, **kw})
+    with pytest.raises(ValueError):
+        Q.qlora_f8_quantize(torch.zeros(4, 4))  # not on a GPU
+    w = Q.F8Matrix.empty(8, 100, Q.QLORA_F8_TILES, device="cpu")
+    with pytest.raises(ValueError):
+        Q.qlora_f8_matmul(q, w)  # 130 against 100
+
+
+@pytest.mark.parametrize("fmt,dtype", [("e4m3", torch.float8_e4m3fn), ("e5m2", torch.float8_e5m2)])
+def test_reference_rounding(fmt, dtype):
+    """round8 against torch's conversion: every code, every midpoint, the values beside it."""
+    mids = torch.from_numpy(R.midpoints(fmt).copy())
+    x = torch.cat([mids, torch.nextafter(mids, torch.tensor(0.0)),
+                   torch.nextafter(mids, torch.tensor(1e9)), torch.zeros(1),
+                   torch.full((1,), R.FMAX[fmt])])
+    x = torch.cat([x, -x])
+    np.testing.assert_array_equal(R.round8(x.numpy(), fmt), x.to(dtype).double().numpy())
