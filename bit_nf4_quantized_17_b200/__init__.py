@@ -5,7 +5,9 @@ kernels behind the C ABI of ``include/qlora.h`` (``libqlora.so``).
 Modules:
 - ``qlora``: the Python binding (argument marshalling only). It covers quantise /
   dequantise, the linear forward and backward (also several adapters per batch
-  and LoRA dropout), merge and unmerge, AdamW with paged states, and timing.
+  and LoRA dropout), merge and unmerge, 8-bit floating point matrices with a scale
+  per block of 128 (kept inputs, their product, a base in 8 bits), AdamW with paged
+  states, and timing.
 - ``dp``: data-parallel replicas (token shards, one flat gradient bucket, one
   all-reduce).
 - ``optim``: ``AdapterAdamW``, the fp32 master weights and moments of one
@@ -20,5 +22,7 @@ from .qlora import (  # noqa: F401
     qlora_linear_bwd, qlora_linear_fwd_multi, qlora_linear_bwd_multi, qlora_linear_fwd_ex,
     qlora_linear_bwd_ex, dropout_keep_mask, qlora_merge, qlora_merge_dense, qlora_adamw,
     qlora_paged_empty, qlora_paged_prefetch, qlora_check, qlora_levels, qlora_nf4_sizes,
-    qlora_linear_workspace, qlora_status_string,
+    qlora_linear_workspace, qlora_status_string, F8Matrix, qlora_f8_sizes, qlora_f8_quantize,
+    qlora_f8_dequantize, qlora_f8_matmul, qlora_linear_bwd_f8, qlora_linear_bwd_f8_workspace,
+    qlora_f8_linear_fwd, qlora_f8_linear_bwd, qlora_f8_linear_workspace,
 )

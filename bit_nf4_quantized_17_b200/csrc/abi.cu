@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "internal.cuh"
+#include "f8.cuh"
 #include "kernels.cuh"
 #include "linear.cuh"
 #include "tc_ptx.cuh"
@@ -479,6 +480,59 @@ qlora_status qlora_linear_bwd_ex(const qlora_nf4* W, const void* A, const void* 
   }
   return linear_backward(*W, *level_table(W->table), A, B, rt, alpha, X, U, dY, M, dX, dA, dB,
                          accumulate != 0, workspace, s, o);
+}
+
+qlora_status qlora_linear_bwd_f8_workspace(int64_t M, int64_t N, int64_t K, int32_t r,
+                                           size_t* bytes) {
+  size_t bwd = 0;
+  const qlora_status st = qlora_linear_workspace(M, N, K, r, nullptr, &bwd);
+  if (st != QLORA_OK) return st;
+  if (bytes) *bytes = align256(bwd) + f8_input_bytes(M, K);
+  return QLORA_OK;
+}
+
+qlora_status qlora_linear_bwd_f8(const qlora_nf4* W, const void* A, const void* B, int32_t r,
+                                 float alpha, const qlora_adapter_opts* opts, const qlora_f8* X8,
+                                 const float* U, const void* dY, void* dX, float* dA, float* dB,
+                                 int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  const NvtxRange nvtx("qlora_linear_bwd_f8");
+  if (!W || !X8 || !workspace) return QLORA_ERR_NULL;
+  qlora_status st = check_f8(*X8);
+  if (st != QLORA_OK) return st;
+  if (X8->layout != QLORA_F8_ROWS) return QLORA_ERR_UNSUPPORTED;
+  if (X8->cols != W->cols) return QLORA_ERR_SHAPE;
+  const int64_t M = X8->rows;
+  // X8 is what the adapter branch read (with dropout the kept form of x_drop),
+  // so no x_drop is asked for: any present pointer satisfies the shared check
+  qlora_adapter_opts x{};
+  if (opts) {
+    x = *opts;
+    if (x.keep_mask) x.x_drop = workspace;
+  }
+  LoraOpts o{};
+  int32_t rt = 0;
+  st = opts_of(opts ? &x : nullptr, W, r, M, &o, &rt);
+  if (st != QLORA_OK) return st;
+  if ((st = check_linear(W, A, B, rt, M, workspace, workspace, workspace_bytes, true)) != QLORA_OK)
+    return st;
+  const size_t base = align256(plan_linear(M, W->rows, W->cols, rt).bwd_workspace);
+  if (workspace_bytes < base + f8_input_bytes(M, W->cols)) return QLORA_ERR_WORKSPACE;
+  if (!dA || !dB || (M > 0 && (!U || !dY))) return QLORA_ERR_NULL;
+  if (!aligned16(dY) || !aligned16(dA) || !aligned16(dB) || !aligned16(dX) || !aligned16(U))
+    return QLORA_ERR_ALIGN;  // (a NULL dX counts as aligned)
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M == 0) {
+    if (accumulate) return QLORA_OK;
+    if (cudaMemsetAsync(dA, 0, sizeof(float) * rt * W->cols, s) != cudaSuccess ||
+        cudaMemsetAsync(dB, 0, sizeof(float) * rt * W->rows, s) != cudaSuccess)
+      return QLORA_ERR_CUDA;
+    return QLORA_OK;
+  }
+  o.x8 = X8;
+  o.x_buf = static_cast<char*>(workspace) + base;
+  return linear_backward(*W, *level_table(W->table), A, B, rt, alpha, nullptr, U, dY, M, dX, dA,
+                         dB, accumulate != 0, workspace, s, o);
 }
 
 qlora_status qlora_linear_fwd_multi(const qlora_nf4* W, const void* A, const void* B,

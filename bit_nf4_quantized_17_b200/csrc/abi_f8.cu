@@ -1,6 +1,7 @@
 // C ABI of the 8-bit operators: argument checks on the host, then launches on
 // the caller's stream.  See include/qlora.h for the contract of each call.
 #include "f8.cuh"
+#include "linear.cuh"
 
 using namespace qlora;
 
@@ -86,6 +87,77 @@ qlora_status qlora_f8_matmul(const qlora_f8* A, const qlora_f8* B, int32_t trans
   if (!aligned16(C)) return QLORA_ERR_ALIGN;
   return f8_gemm(*A, *B, trans_b != 0, C, c_dtype == QLORA_F32, F8Lora{nullptr, nullptr, 0},
                  static_cast<cudaStream_t>(stream));
+}
+
+qlora_status qlora_f8_linear_workspace(int64_t M, int64_t N, int64_t K, int32_t r,
+                                       size_t* fwd_bytes, size_t* bwd_bytes) {
+  if (M < 0 || N < 1 || K < 1 || r < 1 || r > 256 || M > 0x3fffffff || N > 0x7fffffff ||
+      K > 0x7fffff00)
+    return QLORA_ERR_SHAPE;
+  const LinearPlan p = plan_f8_linear(M, N, K, r);
+  if (fwd_bytes) *fwd_bytes = p.fwd_workspace;
+  if (bwd_bytes) *bwd_bytes = p.bwd_workspace;
+  return QLORA_OK;
+}
+
+static qlora_status check_f8_linear(const qlora_f8* W, const void* A, const void* B, int32_t r,
+                                    const qlora_f8* X8, const void* workspace,
+                                    size_t workspace_bytes, bool bwd) {
+  if (!W || !A || !B || !X8 || !workspace) return QLORA_ERR_NULL;
+  qlora_status st = check_f8(*W);
+  if (st != QLORA_OK) return st;
+  if ((st = check_f8(*X8)) != QLORA_OK) return st;
+  if (W->layout != QLORA_F8_TILES || X8->layout != QLORA_F8_ROWS) return QLORA_ERR_UNSUPPORTED;
+  if (W->rows < 1 || X8->cols != W->cols || r < 1 || r > 256 || X8->rows > 0x3fffffff)
+    return QLORA_ERR_SHAPE;
+  // TMA reads bf16 rows of r, N and K elements: multiples of 16 bytes
+  if (r % 8 != 0 || W->rows % 8 != 0 || W->cols % 8 != 0) return QLORA_ERR_UNSUPPORTED;
+  if (!aligned16(A) || !aligned16(B) || !aligned16(workspace)) return QLORA_ERR_ALIGN;
+  const LinearPlan p = plan_f8_linear(X8->rows, W->rows, W->cols, r);
+  if (workspace_bytes < (bwd ? p.bwd_workspace : p.fwd_workspace)) return QLORA_ERR_WORKSPACE;
+  return QLORA_OK;
+}
+
+qlora_status qlora_f8_linear_fwd(const qlora_f8* W, const void* A, const void* B, int32_t r,
+                                 float alpha, const void* X, const qlora_f8* X8, void* Y,
+                                 float* U_save, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  const NvtxRange nvtx("qlora_f8_linear_fwd");
+  const qlora_status st = check_f8_linear(W, A, B, r, X8, workspace, workspace_bytes, false);
+  if (st != QLORA_OK) return st;
+  if (X8->rows == 0) return QLORA_OK;
+  if (!X || !Y) return QLORA_ERR_NULL;
+  if (!aligned16(X) || !aligned16(Y) || !aligned16(U_save)) return QLORA_ERR_ALIGN;
+  return f8_linear_forward(*W, A, B, r, alpha, X, *X8, Y, U_save, workspace,
+                           static_cast<cudaStream_t>(stream));
+}
+
+// No tokens: the gradients of A and B are zero (or stay as they are).
+static qlora_status no_tokens(float* dA, float* dB, int64_t r, int64_t N, int64_t K,
+                              int32_t accumulate, cudaStream_t s) {
+  if (accumulate) return QLORA_OK;
+  if (cudaMemsetAsync(dA, 0, sizeof(float) * r * K, s) != cudaSuccess ||
+      cudaMemsetAsync(dB, 0, sizeof(float) * r * N, s) != cudaSuccess)
+    return QLORA_ERR_CUDA;
+  return QLORA_OK;
+}
+
+qlora_status qlora_f8_linear_bwd(const qlora_f8* W, const void* A, const void* B, int32_t r,
+                                 float alpha, const qlora_f8* X8, const float* U, const void* dY,
+                                 int32_t grad_format, void* dX, float* dA, float* dB,
+                                 int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  const NvtxRange nvtx("qlora_f8_linear_bwd");
+  const qlora_status st = check_f8_linear(W, A, B, r, X8, workspace, workspace_bytes, true);
+  if (st != QLORA_OK) return st;
+  if (grad_format != QLORA_E4M3 && grad_format != QLORA_E5M2) return QLORA_ERR_UNSUPPORTED;
+  if (!dA || !dB || (X8->rows > 0 && (!U || !dY))) return QLORA_ERR_NULL;
+  if (!aligned16(U) || !aligned16(dY) || !aligned16(dX) || !aligned16(dA) || !aligned16(dB))
+    return QLORA_ERR_ALIGN;  // (a NULL dX counts as aligned)
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (X8->rows == 0) return no_tokens(dA, dB, r, W->rows, W->cols, accumulate, s);
+  return f8_linear_backward(*W, A, B, r, alpha, *X8, U, dY, grad_format, dX, dA, dB,
+                            accumulate != 0, workspace, s);
 }
 
 }  // extern "C"

@@ -1,0 +1,177 @@
+// Forward and backward of the linear layer over an 8-bit base weight.
+//
+// The base W (tiles of 128 x 128) takes the place of the NF4 weight; the LoRA
+// branch is the same ("LoRA 与 QLoRA：把大模型微调拆成可负担的工程", 2 and 6):
+//   forward   X^ = 8 bits of X (by rows; kept for the backward), U = X A^T,
+//             Y = X^ W^T + s U B^T
+//   backward  dY^ = 8 bits of dY (by rows), V = dY B, dX = dY^ W + s V A,
+//             dB = s dY^T U, dA = s V^T X^
+// Both large products run on the tensor cores in 8 bits, with the LoRA term as
+// extra bf16 stages of the same accumulators; the rank-r products read X and dY
+// in bf16, except dA, which reads the kept X^.
+#include <algorithm>
+
+#include "f8.cuh"
+#include "linear.cuh"
+
+namespace qlora {
+namespace {
+
+// Workspace (byte offsets; the status word is first).
+//   forward   sU [hi | lo]
+//   backward  sV [hi | lo] | V (fp32, few tokens) or V^T [hi ; lo] | U^T [hi ; lo] |
+//             dY codes | dY scales | split-K partials (ranks above 128) | X^ in bf16
+struct Layout {
+  size_t su, fwd_end;
+  size_t sv, vt, ut, dy_codes, dy_scales, part, x_buf, bwd_end;
+  int64_t dy_ld;
+  int split_db, split_da;
+};
+
+Layout layout(int64_t M, int64_t N, int64_t K, int32_t r) {
+  Layout L{};
+  if (M < 1) M = 1;  // no tokens: no work, but a workspace with a status word
+  const int64_t span = lora_span(r), r16 = lora_rows(r), mp = pad8(M);
+  L.su = kStatusBytes;
+  L.fwd_end = L.su + align256(2 * M * 2 * span);
+  L.sv = kStatusBytes;
+  L.vt = L.sv + align256(2 * M * 2 * span);
+  L.ut = L.vt + align256(std::max<size_t>(2 * 2 * r16 * mp, sizeof(float) * M * r));
+  L.dy_codes = L.ut + align256(2 * 2 * r16 * mp);
+  L.dy_ld = ceil_div(N, 16) * 16;
+  L.dy_scales = L.dy_codes + align256(M * L.dy_ld);
+  L.part = L.dy_scales + align256(sizeof(float) * f8_blocks(N) * M);
+  L.split_db = tc_split_count(ceil_div(N, 128), ceil_div(M, 64));
+  L.split_da = tc_split_count(ceil_div(K, 128), ceil_div(M, 64));
+  const bool one_launch = 2 * r16 <= 256;
+  L.x_buf = L.part + (one_launch ? 0
+                                 : align256(sizeof(float) * 2 * r16 *
+                                            std::max(L.split_db * N, L.split_da * K)));
+  L.bwd_end = L.x_buf + f8_input_bytes(M, K);
+  return L;
+}
+
+}  // namespace
+
+LinearPlan plan_f8_linear(int64_t M, int64_t N, int64_t K, int32_t r) {
+  const Layout L = layout(M, N, K, r);
+  return LinearPlan{L.fwd_end, L.bwd_end};
+}
+
+qlora_status f8_linear_forward(const qlora_f8& W, const void* A, const void* B, int32_t r,
+                               float alpha, const void* X, const qlora_f8& x8, void* Y,
+                               float* U_save, void* workspace, cudaStream_t s) {
+  const int64_t M = x8.rows, N = W.rows, K = W.cols;
+  const Layout L = layout(M, N, K, r);
+  const float sc = lora_scale(alpha, r);
+  const int32_t r16 = lora_rows(r), span = lora_span(r);
+  char* ws = static_cast<char*>(workspace);
+  auto* st = reinterpret_cast<DeviceStatus*>(ws);
+  char* su = ws + L.su;
+  QLORA_TRY(launch_f8_quantize(X, QLORA_BF16, x8, s));
+  // U = X A^T -> U_save (fp32) and sU = s U as bf16 hi + lo
+  if (M <= kSmallM) {
+    const RankOut ro{r, U_save, r, 1.0f, reinterpret_cast<__nv_bfloat16*>(su), 2 * span,
+                     sc, span, nullptr, r};
+    QLORA_TRY(rank_down(X, A, static_cast<int>(M), K, span, ro, s));
+  } else {
+    ReduceArgs ra = reduce_args(nullptr, 1, M, r, r16);
+    ra.o1 = U_save;
+    ra.ld1 = r;
+    ra.a1 = 1.0f;
+    ra.o2 = su;
+    ra.ld2 = 2 * span;
+    ra.a2 = sc;
+    ra.o2_lo = span;
+    ra.o2_pad = 1;
+    QLORA_TRY(tc_rank_gemm(X, false, M, K, K, A, false, K, r, r16, ra, st, s));
+  }
+  return f8_gemm(x8, W, true, Y, false, F8Lora{su, B, r}, s);
+}
+
+qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B, int32_t r,
+                                float alpha, const qlora_f8& x8, const float* U, const void* dY,
+                                int32_t grad_format, void* dX, float* dA, float* dB,
+                                bool accumulate, void* workspace, cudaStream_t s) {
+  const int64_t M = x8.rows, N = W.rows, K = W.cols;
+  const Layout L = layout(M, N, K, r);
+  const float sc = lora_scale(alpha, r);
+  const int32_t r16 = lora_rows(r), span = lora_span(r);
+  const int64_t mp = pad8(M);
+  char* ws = static_cast<char*>(workspace);
+  auto* st = reinterpret_cast<DeviceStatus*>(ws);
+  char *sv = ws + L.sv, *vt = ws + L.vt, *ut = ws + L.ut;
+  float* v = reinterpret_cast<float*>(vt);  // few tokens: V in fp32
+  float* part = reinterpret_cast<float*>(ws + L.part);
+  void* xb = ws + L.x_buf;
+  const bool small = M <= kSmallM;
+  // V = dY B -> sV = s V as [hi | lo], and V (fp32) or V^T as [hi ; lo]
+  if (small) {
+    const RankOut rv{r, v, r, 1.0f, reinterpret_cast<__nv_bfloat16*>(sv), 2 * span,
+                     sc, span, nullptr, r};
+    QLORA_TRY(rank_v(dY, B, static_cast<int>(M), N, span, rv, s));
+  } else {
+    ReduceArgs ra = reduce_args(nullptr, 1, M, r, r16);
+    ra.o2 = sv;
+    ra.ld2 = 2 * span;
+    ra.a2 = sc;
+    ra.o2_lo = span;
+    ra.o2_pad = 1;
+    ra.o3 = vt;
+    ra.ld3 = mp;
+    ra.a3 = 1.0f;
+    ra.o3_lo = r16;
+    QLORA_TRY(tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s));
+  }
+  // dB and dA on the side stream, dX on the caller's: they share only inputs
+  SideStream* ss = nullptr;
+  QLORA_TRY(side_stream(&ss));
+  const cudaStream_t s2 = ss->stream;
+  if (cudaEventRecord(ss->fork, s) != cudaSuccess ||
+      cudaStreamWaitEvent(s2, ss->fork, 0) != cudaSuccess)
+    return QLORA_ERR_CUDA;
+  auto main_work = [&]() -> qlora_status {
+    if (!dX) return QLORA_OK;
+    const qlora_f8 dy8{M, N, L.dy_ld, QLORA_F8_ROWS, grad_format, x8.pow2, 0,
+                       reinterpret_cast<uint8_t*>(ws + L.dy_codes),
+                       reinterpret_cast<float*>(ws + L.dy_scales)};
+    QLORA_TRY(launch_f8_quantize(dY, QLORA_BF16, dy8, s));
+    return f8_gemm(dy8, W, false, dX, false, F8Lora{sv, A, r}, s);
+  };
+  auto side_work = [&]() -> qlora_status {
+    QLORA_TRY(launch_f8_dequantize(x8, xb, QLORA_BF16, s2));
+    if (small) {
+      const int m = static_cast<int>(M);
+      QLORA_TRY(small_grad_b(dY, U, m, N, r, sc, accumulate, dB, s2));
+      return small_grad_a(v, xb, m, K, r, sc, accumulate, dA, s2);
+    }
+    QLORA_TRY(transpose_to_bf16(U, true, M, r, r, ut, mp, r16, s2));
+    ReduceArgs rb = reduce_args(part, L.split_db, N, r, 2 * r16);
+    rb.lo = r16;
+    rb.o1 = dB;
+    rb.ld1 = r;
+    rb.a1 = sc;
+    rb.acc1 = accumulate;
+    QLORA_TRY(rank_product(dY, true, N, M, N, ut, mp, 2 * r16, 2 * r16, part, L.split_db, rb, st,
+                           s2));
+    ReduceArgs ra = reduce_args(part, L.split_da, K, r, 2 * r16);
+    ra.lo = r16;
+    ra.o1 = dA;
+    ra.ld1 = K;
+    ra.trans1 = true;
+    ra.a1 = sc;
+    ra.acc1 = accumulate;
+    return rank_product(xb, true, K, M, K, vt, mp, 2 * r16, 2 * r16, part, L.split_da, ra, st,
+                        s2);
+  };
+  const qlora_status st_main = main_work();
+  const qlora_status st_side = side_work();
+  // join on every path, so that nothing of this call runs past it on the side stream
+  const bool joined = cudaEventRecord(ss->join, s2) == cudaSuccess &&
+                      cudaStreamWaitEvent(s, ss->join, 0) == cudaSuccess;
+  if (st_side != QLORA_OK) return st_side;
+  if (st_main != QLORA_OK) return st_main;
+  return joined ? QLORA_OK : QLORA_ERR_CUDA;
+}
+
+}  // namespace qlora

@@ -29,13 +29,12 @@
 // Other shapes take the CUDA-core contraction of gemm_simt.cu.
 #include <algorithm>
 
+#include "f8.cuh"
 #include "kernels.cuh"
 #include "linear.cuh"
 
 namespace qlora {
 namespace {
-
-size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
 
 QView view_of(const qlora_nf4& W) {
   return QView{W.codes, W.scale_codes, W.factors, W.mean, W.rows, W.cols,
@@ -43,14 +42,10 @@ QView view_of(const qlora_nf4& W) {
                __builtin_ctz(W.blocksize) - 6};
 }
 
-float lora_scale(float alpha, int32_t r) { return alpha / static_cast<float>(r); }
-
 bool use_tc(int64_t M, int64_t N, int64_t K, int32_t r) {
   (void)K;
   return M >= 1 && M < (int64_t(1) << 30) && N % 8 == 0 && r % 8 == 0;
 }
-
-int64_t pad8(int64_t v) { return (v + 7) / 8 * 8; }
 
 struct TcSplits {
   int u, v, db, da;
@@ -122,16 +117,13 @@ SmallLayout small_layout(int64_t M, int64_t N, int64_t K, int32_t r) {
 
 bool use_small(int64_t M) { return M <= kSmallM; }
 
+}  // namespace
+
 // A second stream for the part of the backward pass that does not feed the
 // fused dX kernel (dB, dA): launched after V is ready, it runs on the SMs that
 // kernel leaves idle in its last wave.  One per host thread and device; the
 // caller's stream waits for it before the call returns, so every call stays
 // ordered on the caller's stream (and can be captured in a CUDA graph).
-struct SideStream {
-  cudaStream_t stream = nullptr;
-  cudaEvent_t fork = nullptr, join = nullptr;
-};
-
 qlora_status side_stream(SideStream** out) {
   constexpr int kMaxDevices = 64;
   thread_local SideStream per_device[kMaxDevices];
@@ -177,8 +169,6 @@ qlora_status rank_product(const void* A, bool a_mn, int64_t m_rows, int64_t kdim
   return splitk_reduce(ra, s);
 }
 
-}  // namespace
-
 LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, int32_t r) {
   LinearPlan p;
   if (use_tc(M, N, K, r) && use_small(M)) {
@@ -199,11 +189,7 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, int32_t r) {
   return p;
 }
 
-#define QLORA_TRY(x)                      \
-  do {                                    \
-    qlora_status _st = (x);               \
-    if (_st != QLORA_OK) return _st;      \
-  } while (0)
+size_t f8_input_bytes(int64_t M, int64_t K) { return align256(2 * M * K); }
 
 bool linear_multi_supported(int64_t M, int64_t N, int64_t K, int32_t r) {
   return use_tc(M > 0 ? M : 1, N, K, r);  // (M = 0 is a no-op on every path)
@@ -298,7 +284,7 @@ qlora_status linear_backward(const qlora_nf4& W, const LevelTable& t, const void
   // with dropout the adapter branch saw X (.) D: dA and a recomputed U read it,
   // the LoRA stage of the dX GEMM is switched off (sV = 0) and the masked
   // term D (.) s V A / (1 - p) is added to dX afterwards
-  const void* xl = o.mask ? o.x_drop : X;
+  const void* xl = o.x8 ? o.x_buf : (o.mask ? o.x_drop : X);
   const float sc_dx = o.mask ? 0.0f : sc;
   const QView w = view_of(W);
   char* ws = static_cast<char*>(workspace);
@@ -359,6 +345,7 @@ qlora_status linear_backward(const qlora_nf4& W, const LevelTable& t, const void
     };
     auto side_work = [&]() -> qlora_status {
       QLORA_TRY(small_grad_b(dY, U, m, N, r, sc, accumulate, dB, s2));
+      if (o.x8) QLORA_TRY(launch_f8_dequantize(*o.x8, o.x_buf, QLORA_BF16, s2));
       return small_grad_a(v, xl, m, K, r, sc * o.keep, accumulate, dA, s2);
     };
     // the dX kernel is enqueued first so that it takes the SMs
@@ -446,6 +433,7 @@ qlora_status linear_backward(const qlora_nf4& W, const LevelTable& t, const void
         QLORA_TRY(rank_product(dY, true, N, M, N, ut, mp, 2 * r16, 2 * r16, part, sp.db, ra, st,
                                s2));
       }
+      if (o.x8) QLORA_TRY(launch_f8_dequantize(*o.x8, o.x_buf, QLORA_BF16, s2));
       // dA = s V^T X: rows d_in, stored transposed as r x d_in
       ReduceArgs ra = reduce_args(part, sp.da, K, r, 2 * r16);
       ra.lo = r16;
@@ -510,8 +498,9 @@ qlora_status linear_backward(const qlora_nf4& W, const LevelTable& t, const void
   // dB = s dY^T U (+ dB)   element (n, m) of dY^T = dY[m][n]; element (j, m) of U^T = U[m][j]
   QLORA_TRY(simt_gemm(OP_BF16_MN, dense(dY, N), OP_F32_MN, dense(U, r), N, r, M, sc,
                       accumulate ? dB : nullptr, dB, r, false, t, s));
+  if (o.x8) QLORA_TRY(launch_f8_dequantize(*o.x8, o.x_buf, QLORA_BF16, s));
   // dA = s V^T X (+ dA)
-  return simt_gemm(OP_F32_MN, dense(v, r), OP_BF16_MN, dense(X, K), r, K, M, sc,
+  return simt_gemm(OP_F32_MN, dense(v, r), OP_BF16_MN, dense(xl, K), r, K, M, sc,
                    accumulate ? dA : nullptr, dA, K, false, t, s);
 }
 

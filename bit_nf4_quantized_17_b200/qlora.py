@@ -118,6 +118,14 @@ def lib():
             "qlora_f8_quantize": (ctypes.c_int, [vp, i32, pf, vp]),
             "qlora_f8_dequantize": (ctypes.c_int, [pf, vp, i32, vp]),
             "qlora_f8_matmul": (ctypes.c_int, [pf, pf, i32, vp, i32, vp]),
+            "qlora_linear_bwd_f8_workspace": (ctypes.c_int, [i64, i64, i64, i32, psz]),
+            "qlora_linear_bwd_f8": (ctypes.c_int, [pq, vp, vp, i32, f32, po, pf, vp, vp, vp, vp,
+                                                   vp, i32, vp, sz, vp]),
+            "qlora_f8_linear_workspace": (ctypes.c_int, [i64, i64, i64, i32, psz, psz]),
+            "qlora_f8_linear_fwd": (ctypes.c_int, [pf, vp, vp, i32, f32, vp, pf, vp, vp, vp, sz,
+                                                   vp]),
+            "qlora_f8_linear_bwd": (ctypes.c_int, [pf, vp, vp, i32, f32, pf, vp, vp, i32, vp, vp,
+                                                   vp, i32, vp, sz, vp]),
             "qlora_check": (ctypes.c_int, [vp, vp]),
             "qlora_selftest_timeout": (ctypes.c_int, [i64, vp, vp]),
             "qlora_merge": (ctypes.c_int, [pq, vp, vp, i32, f32, vp, vp]),
@@ -619,6 +627,114 @@ def qlora_f8_matmul(a, b, trans_b=True, dtype=torch.bfloat16, out=None, stream=N
     _ok(lib().qlora_f8_matmul(a.struct, b.struct, 1 if trans_b else 0, out.data_ptr(),
                               _DTYPE[out.dtype], _stream(stream)), "qlora_f8_matmul")
     return out
+
+
+def qlora_linear_bwd_f8_workspace(M, N, K, r):
+    b = ctypes.c_size_t()
+    _ok(lib().qlora_linear_bwd_f8_workspace(M, N, K, r, ctypes.byref(b)),
+        "qlora_linear_bwd_f8_workspace")
+    return b.value
+
+
+def _grads(M, N, K, r, device, want_dx, dX, dA, dB, stream):
+    with _in_stream(stream):
+        if want_dx and dX is None:
+            dX = torch.empty((M, K), dtype=torch.bfloat16, device=device)
+        if dA is None:
+            dA = torch.empty((r, K), dtype=torch.float32, device=device)
+        if dB is None:
+            dB = torch.empty((N, r), dtype=torch.float32, device=device)
+    return (dX if want_dx else None), dA, dB
+
+
+def qlora_linear_bwd_f8(q, A, B, r, alpha, X8, U, dY, adapter=None, p=0.0, keep_mask=None,
+                        dX=None, dA=None, dB=None, accumulate=False, want_dx=True,
+                        workspace=None, stream=None, check=False):
+    """qlora_linear_bwd_ex with the input kept in 8 bits (X8 = qlora_f8_quantize(X), with
+    dropout of x_drop) in the place of X.  Returns (dX, dA, dB)."""
+    M, rt, dev = X8.rows, A.shape[0], X8.codes.device
+    if X8.layout != QLORA_F8_ROWS or X8.cols != q.cols:
+        raise ValueError(f"X8: expected {q.cols} columns held by rows, got {X8.cols}"
+                         f"{'' if X8.layout == QLORA_F8_ROWS else ' held by tiles'}")
+    if U is None:
+        raise ValueError("U: the forward's X A^T is needed, X is not kept")
+    dX, dA, dB = _grads(M, q.rows, q.cols, rt, dev, want_dx, dX, dA, dB, stream)
+    o = _opts(r, A, adapter, p, keep_mask, None)
+    _check_linear(q, M, rt, A=A, B=B, U=U, dY=dY, dX=dX, dA=dA, dB=dB, adapter=adapter,
+                  keep_mask=keep_mask)
+    _on_current_device(q.codes, X8.codes, A, B, U, dY, dX, dA, dB, adapter, keep_mask, workspace)
+    if workspace is None:
+        with _in_stream(stream):
+            workspace = _workspace(qlora_linear_bwd_f8_workspace(M, q.rows, q.cols, rt), dev)
+    _ok(lib().qlora_linear_bwd_f8(q.struct, _ptr(A), _ptr(B), r, float(alpha), o, X8.struct,
+                                  _ptr(U), _ptr(dY), _ptr(dX), _ptr(dA), _ptr(dB),
+                                  1 if accumulate else 0, _ptr(workspace), workspace.numel(),
+                                  _stream(stream)), "qlora_linear_bwd_f8")
+    if check:
+        qlora_check(workspace, stream)
+    return dX, dA, dB
+
+
+def qlora_f8_linear_workspace(M, N, K, r):
+    f, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _ok(lib().qlora_f8_linear_workspace(M, N, K, r, ctypes.byref(f), ctypes.byref(b)),
+        "qlora_f8_linear_workspace")
+    return f.value, b.value
+
+
+def _check_f8_base(W, X8):
+    if W.layout != QLORA_F8_TILES:
+        raise ValueError("W: expected a weight held by tiles")
+    if X8.layout != QLORA_F8_ROWS or X8.cols != W.cols:
+        raise ValueError(f"X8: expected {W.cols} columns held by rows, got {X8.cols}"
+                         f"{'' if X8.layout == QLORA_F8_ROWS else ' held by tiles'}")
+
+
+def qlora_f8_linear_fwd(W, A, B, alpha, X, X8, Y=None, U_save=None, workspace=None, stream=None,
+                        check=False):
+    """The linear layer over an 8-bit base W (an F8Matrix by tiles): Y = X^ W^T + (alpha/r)
+    (X A^T) B^T.  X8 (an F8Matrix by rows, e.g. F8Matrix.empty(M, d_in)) receives the 8 bits
+    of X and is what the backward takes.  Returns Y."""
+    M, r = X8.rows, A.shape[0]
+    _check_f8_base(W, X8)
+    if Y is None:
+        with _in_stream(stream):
+            Y = torch.empty((M, W.rows), dtype=torch.bfloat16, device=X.device)
+    _check_linear(W, M, r, A=A, B=B, X=X, Y=Y, U=U_save)
+    _on_current_device(W.codes, A, B, X, X8.codes, Y, U_save, workspace)
+    if workspace is None:
+        with _in_stream(stream):
+            workspace = _workspace(qlora_f8_linear_workspace(M, W.rows, W.cols, r)[0], X.device)
+    _ok(lib().qlora_f8_linear_fwd(W.struct, _ptr(A), _ptr(B), r, float(alpha), _ptr(X), X8.struct,
+                                  _ptr(Y), _ptr(U_save), _ptr(workspace), workspace.numel(),
+                                  _stream(stream)), "qlora_f8_linear_fwd")
+    if check:
+        qlora_check(workspace, stream)
+    return Y
+
+
+def qlora_f8_linear_bwd(W, A, B, alpha, X8, U, dY, grad_format=QLORA_E5M2, dX=None, dA=None,
+                        dB=None, accumulate=False, want_dx=True, workspace=None, stream=None,
+                        check=False):
+    """Backward of qlora_f8_linear_fwd from the kept X8; dY goes into 8 bits of grad_format
+    for dX = dY^ W + (alpha/r) (dY B) A.  Returns (dX, dA, dB)."""
+    M, r, dev = X8.rows, A.shape[0], X8.codes.device
+    _check_f8_base(W, X8)
+    if U is None:
+        raise ValueError("U: the forward's X A^T is needed, X is not kept")
+    dX, dA, dB = _grads(M, W.rows, W.cols, r, dev, want_dx, dX, dA, dB, stream)
+    _check_linear(W, M, r, A=A, B=B, U=U, dY=dY, dX=dX, dA=dA, dB=dB)
+    _on_current_device(W.codes, X8.codes, A, B, U, dY, dX, dA, dB, workspace)
+    if workspace is None:
+        with _in_stream(stream):
+            workspace = _workspace(qlora_f8_linear_workspace(M, W.rows, W.cols, r)[1], dev)
+    _ok(lib().qlora_f8_linear_bwd(W.struct, _ptr(A), _ptr(B), r, float(alpha), X8.struct, _ptr(U),
+                                  _ptr(dY), int(grad_format), _ptr(dX), _ptr(dA), _ptr(dB),
+                                  1 if accumulate else 0, _ptr(workspace), workspace.numel(),
+                                  _stream(stream)), "qlora_f8_linear_bwd")
+    if check:
+        qlora_check(workspace, stream)
+    return dX, dA, dB
 
 
 class _PagedBlock:

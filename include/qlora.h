@@ -356,6 +356,48 @@ qlora_status qlora_f8_dequantize(const qlora_f8* q, void* X_out, int32_t out_dty
 qlora_status qlora_f8_matmul(const qlora_f8* A, const qlora_f8* B, int32_t trans_b, void* C,
                              int32_t c_dtype, void* stream);
 
+/* Backward pass of the NF4 layer (qlora_linear_bwd_ex) whose input was kept in 8 bits
+ * instead of bf16, half the bytes that a layer keeps from its forward to its backward:
+ * X8 = qlora_f8_quantize(X), layout QLORA_F8_ROWS, gives the token count (its rows)
+ * and takes the place of X in dA = s V^T X^, X^ = bf16(code * s) (what
+ * qlora_f8_dequantize writes).  With dropout X8 is the kept form of the forward's x_drop,
+ * and opts->x_drop is not read.  U (M x r fp32) from the forward is required.  dX and
+ * dB do not depend on X.  opts may be NULL: one adapter, no dropout.  Workspace: at
+ * least the bytes of qlora_linear_bwd_f8_workspace (rank n_adapters r).  Errors as
+ * qlora_linear_bwd_ex and qlora_f8_quantize. */
+qlora_status qlora_linear_bwd_f8_workspace(int64_t M, int64_t N, int64_t K, int32_t r,
+                                           size_t* bytes);
+qlora_status qlora_linear_bwd_f8(const qlora_nf4* W, const void* A, const void* B, int32_t r,
+                                 float alpha, const qlora_adapter_opts* opts, const qlora_f8* X8,
+                                 const float* U, const void* dY, void* dX, float* dA, float* dB,
+                                 int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* The linear layer over an 8-bit base: W (d_out x d_in, layout QLORA_F8_TILES, e.g. a
+ * merged weight through qlora_f8_quantize) in the place of the NF4 weight, the same LoRA
+ * branch, the large products on the tensor cores in 8 bits:
+ *   fwd  X8 = 8 bits of X (its arrays are the caller's; X8->rows is the token count; kept
+ *        for the backward, where it stands in for X), U = X A^T,
+ *        Y = X^ W^T + s U B^T
+ *   bwd  dY^ = 8 bits of dY (grad_format, layout QLORA_F8_ROWS, pow2 as X8), V = dY B,
+ *        dX = dY^ W + s V A,  dB = s dY^T U,  dA = s V^T bf16(X^)
+ * X, dY, Y, dX: bf16; A, B: bf16; U_save / U, dA, dB: fp32, as in the NF4 layer.  dX and
+ * U_save may be NULL.  dA and dB are overwritten, or added to when accumulate != 0.
+ * Requirements: r, d_out and d_in multiples of 8 (else QLORA_ERR_UNSUPPORTED),
+ * 1 <= r <= 256, X8 of layout QLORA_F8_ROWS with d_in columns.  A workspace from
+ * qlora_f8_linear_workspace, zero-filled before its first use, holds the status word. */
+qlora_status qlora_f8_linear_workspace(int64_t M, int64_t N, int64_t K, int32_t r,
+                                       size_t* fwd_bytes, size_t* bwd_bytes);
+qlora_status qlora_f8_linear_fwd(const qlora_f8* W, const void* A, const void* B, int32_t r,
+                                 float alpha, const void* X, const qlora_f8* X8, void* Y,
+                                 float* U_save, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+qlora_status qlora_f8_linear_bwd(const qlora_f8* W, const void* A, const void* B, int32_t r,
+                                 float alpha, const qlora_f8* X8, const float* U, const void* dY,
+                                 int32_t grad_format, void* dX, float* dA, float* dB,
+                                 int32_t accumulate, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
 /* Paged optimiser states.  The optimiser moments can live in CUDA managed
  * (unified) memory, which the driver migrates between host and device pages
  * on demand, so that they need not stay in HBM ("LoRA 与 QLoRA：把大模型微调

@@ -85,6 +85,79 @@ def test_call_refusals():
     assert L.qlora_f8_matmul(empty, b, 1, None, 0, None) == Q.QLORA_OK
 
 
+def _lin(L, bwd, W=None, A=BUF, B=BUF, r=16, x8=None, X=BUF, U=BUF, Y=BUF, dA=BUF, dB=BUF,
+         grad=Q.QLORA_E5M2, ws=BUF, nbytes=1 << 30):
+    W = W if W is not None else _m(256, 128, Q.QLORA_F8_TILES)
+    x8 = x8 if x8 is not None else _m(32, 128)
+    if bwd:
+        return L.qlora_f8_linear_bwd(W, A, B, r, 1.0, x8, U, Y, grad, X, dA, dB, 0, ws, nbytes,
+                                     None)
+    return L.qlora_f8_linear_fwd(W, A, B, r, 1.0, X, x8, Y, U, ws, nbytes, None)
+
+
+def test_linear_refusals():
+    L = Q.lib()
+    both = [
+        (dict(A=None), Q.QLORA_ERR_NULL), (dict(B=None), Q.QLORA_ERR_NULL),
+        (dict(ws=None), Q.QLORA_ERR_NULL), (dict(Y=None), Q.QLORA_ERR_NULL),
+        (dict(A=BUF + 8), Q.QLORA_ERR_ALIGN), (dict(U=BUF + 4), Q.QLORA_ERR_ALIGN),
+        (dict(ws=BUF + 8), Q.QLORA_ERR_ALIGN), (dict(X=BUF + 2), Q.QLORA_ERR_ALIGN),
+        (dict(r=0), Q.QLORA_ERR_SHAPE), (dict(r=257), Q.QLORA_ERR_SHAPE),
+        (dict(r=12), Q.QLORA_ERR_UNSUPPORTED),
+        (dict(W=_m(252, 128, Q.QLORA_F8_TILES)), Q.QLORA_ERR_UNSUPPORTED),
+        (dict(W=_m(256, 124, Q.QLORA_F8_TILES, ld=128), x8=_m(32, 124, ld=128)),
+         Q.QLORA_ERR_UNSUPPORTED),
+        (dict(W=_m(256, 128)), Q.QLORA_ERR_UNSUPPORTED),
+        (dict(x8=_m(32, 128, Q.QLORA_F8_TILES)), Q.QLORA_ERR_UNSUPPORTED),
+        (dict(x8=_m(32, 256)), Q.QLORA_ERR_SHAPE),
+        (dict(W=_m(0, 128, Q.QLORA_F8_TILES)), Q.QLORA_ERR_SHAPE),
+        (dict(nbytes=256), Q.QLORA_ERR_WORKSPACE),
+    ]
+    for bwd in (False, True):
+        for kw, status in both:
+            assert _lin(L, bwd, **kw) == status, (bwd, kw)
+    assert _lin(L, False, X=None) == Q.QLORA_ERR_NULL
+    for kw, status in ((dict(U=None), Q.QLORA_ERR_NULL), (dict(dA=None), Q.QLORA_ERR_NULL),
+                       (dict(dB=None), Q.QLORA_ERR_NULL), (dict(dA=BUF + 8), Q.QLORA_ERR_ALIGN),
+                       (dict(grad=2), Q.QLORA_ERR_UNSUPPORTED)):
+        assert _lin(L, True, **kw) == status, kw
+    assert _lin(L, False, x8=_m(0, 128, codes=None, scales=None)) == Q.QLORA_OK
+
+
+def test_kept_input_refusals():
+    L = Q.lib()
+
+    def call(q=None, x8=None, r=16, U=BUF, dY=BUF, dA=BUF, dB=BUF, ws=BUF, nbytes=1 << 30, opts=None):
+        q = q or Q.qlora_nf4(256, 128, 64, 256, 0, 0, BUF, BUF, BUF, BUF)
+        return L.qlora_linear_bwd_f8(q, BUF, BUF, r, 1.0, opts, x8 or _m(32, 128), U, dY, BUF, dA,
+                                     dB, 0, ws, nbytes, None)
+    for kw, status in ((dict(U=None), Q.QLORA_ERR_NULL), (dict(dY=None), Q.QLORA_ERR_NULL),
+                       (dict(dA=None), Q.QLORA_ERR_NULL), (dict(ws=None), Q.QLORA_ERR_NULL),
+                       (dict(dB=BUF + 8), Q.QLORA_ERR_ALIGN), (dict(r=0), Q.QLORA_ERR_SHAPE),
+                       (dict(x8=_m(32, 256)), Q.QLORA_ERR_SHAPE),
+                       (dict(x8=_m(32, 128, Q.QLORA_F8_TILES)), Q.QLORA_ERR_UNSUPPORTED),
+                       (dict(x8=_m(32, 128, codes=None)), Q.QLORA_ERR_NULL),
+                       (dict(nbytes=Q.qlora_linear_bwd_f8_workspace(32, 256, 128, 16) - 1),
+                        Q.QLORA_ERR_WORKSPACE),
+                       (dict(opts=Q.qlora_adapter_opts(2, 0, None, 0.0, 0, None, None)),
+                        Q.QLORA_ERR_NULL),
+                       (dict(opts=Q.qlora_adapter_opts(1, 0, None, 1.0, 0, BUF, None)),
+                        Q.QLORA_ERR_UNSUPPORTED)):
+        assert call(**kw) == status, kw
+
+
+def test_workspace_queries():
+    for M in (0, 1, 16, 17, 5000):
+        f, b = Q.qlora_f8_linear_workspace(M, 256, 128, 16)
+        assert 256 <= f <= b
+        assert Q.qlora_linear_bwd_f8_workspace(M, 256, 128, 16) >= \
+            Q.qlora_linear_workspace(M, 256, 128, 16)[1] + 2 * M * 128
+    for args in ((-1, 8, 8, 8), (1, 0, 8, 8), (1, 8, 8, 257), (1 << 30, 8, 8, 8)):
+        with pytest.raises(Q.QloraError) as e:
+            Q.qlora_f8_linear_workspace(*args)
+        assert e.value.status == Q.QLORA_ERR_SHAPE
+
+
 def test_binding_refusals():
     u8 = torch.uint8
     good = dict(rows=4, cols=130, layout=Q.QLORA_F8_ROWS, format=Q.QLORA_E4M3, pow2=False,
