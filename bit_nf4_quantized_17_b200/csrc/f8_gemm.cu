@@ -30,32 +30,17 @@
 
 #include <algorithm>
 
-#include "f8.cuh"
-#include "tc_common.cuh"
-#include "tc_ptx.cuh"
+#include "f8_gemm.cuh"
 
 namespace qlora {
 namespace {
 
-constexpr long long kTimeoutCycles = 4000000000ll;  // ~2 s at 1.9 GHz
+using f8::GemmArgs;
+using f8::kTimeoutCycles;
+using f8::store_run;
+
 constexpr int kPBytes = 16384;                      // 128 rows x 128 bytes
 constexpr int kMaxStages = 12;
-
-struct GemmArgs {
-  int32_t m, n;                // rows (tokens) and columns of C
-  int32_t kb_total, kb_per;    // 128-deep blocks, blocks per split
-  int32_t n_tiles;             // tiles along the P x Q grid's fast axis
-  int32_t stages;
-  int32_t b_mn;                // B MN-major: its contraction axis is its rows
-  int32_t ext_tiles, ext_half, ext_last_steps, ext_mn;
-  int32_t c_f32;
-  const float* sa;             // A's scales, [kb][m]
-  const float* sb;             // B's scales: block column nb at sb[nb * sb_n + kb * sb_k]
-  int64_t sb_n, sb_k;
-  void* c;
-  int64_t c_ld;
-  uint32_t idesc, idesc_ext;
-};
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   float4 v;
@@ -63,45 +48,6 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(addr));
   return v;
-}
-
-// N consecutive columns of a row of C from column c0 (N = 4 or 16)
-template <int N>
-__device__ __forceinline__ void store_run(const GemmArgs& p, int64_t row, int64_t c0,
-                                          const float* v) {
-  if (row >= p.m || c0 >= p.n) return;
-  const int64_t at = row * p.c_ld + c0;
-  const bool whole = c0 + N <= p.n;
-  if (p.c_f32) {
-    float* o = static_cast<float*>(p.c) + at;
-    if (whole && (p.c_ld & 3) == 0) {
-#pragma unroll
-      for (int j = 0; j < N; j += 4)
-        *reinterpret_cast<float4*>(o + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (c0 + j < p.n) o[j] = v[j];
-    }
-  } else {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.c) + at;
-    if (whole && N == 16 && (p.c_ld & 7) == 0) {
-      uint32_t w[N / 2];
-#pragma unroll
-      for (int j = 0; j < N / 2; ++j) w[j] = tc::pack_bf16x2(v[2 * j], v[2 * j + 1]);
-#pragma unroll
-      for (int j = 0; j < N / 8; ++j)
-        reinterpret_cast<uint4*>(o)[j] =
-            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-    } else if (whole && N == 4 && (p.c_ld & 3) == 0) {
-      *reinterpret_cast<uint2*>(o) =
-          make_uint2(tc::pack_bf16x2(v[0], v[1]), tc::pack_bf16x2(v[2], v[3]));
-    } else {
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (c0 + j < p.n) o[j] = __float2bfloat16_rn(v[j]);
-    }
-  }
 }
 
 template <int BN, bool SWAP>
@@ -482,8 +428,8 @@ int split_count(int64_t tiles, int64_t kb) {
 
 }  // namespace
 
-qlora_status f8_gemm(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,
-                     const F8Lora& l, cudaStream_t s) {
+f8::GemmArgs f8::gemm_args(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,
+                           const F8Lora& l) {
   GemmArgs p{};
   p.m = static_cast<int32_t>(a.rows);
   p.n = static_cast<int32_t>(trans_b ? b.rows : b.cols);
@@ -503,6 +449,12 @@ qlora_status f8_gemm(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c
     p.ext_last_steps = ((l.r - 64 * (p.ext_half - 1)) + 15) / 16;
     p.ext_mn = trans_b ? 0 : 1;
   }
+  return p;
+}
+
+qlora_status f8_gemm(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,
+                     const F8Lora& l, cudaStream_t s) {
+  const GemmArgs p = f8::gemm_args(a, b, trans_b, c, c_f32, l);
   const int64_t m = p.m, n = p.n;
   if (m <= 64) {
     const int splits = split_count(ceil_div(n, 128), p.kb_total);
@@ -510,8 +462,9 @@ qlora_status f8_gemm(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c
     if (m <= 32) return launch<32, true>(a, b, trans_b, p, l, splits, s);
     return launch<64, true>(a, b, trans_b, p, l, splits, s);
   }
-  const int splits = split_count(ceil_div(n, 128) * ceil_div(m, 128), p.kb_total);
-  return launch<128, false>(a, b, trans_b, p, l, splits, s);
+  const int64_t tiles = ceil_div(n, 128) * ceil_div(m, 128);
+  if (tiles > 148) return f8_gemm_pairs(a, b, trans_b, c, c_f32, l, s);
+  return launch<128, false>(a, b, trans_b, p, l, split_count(tiles, p.kb_total), s);
 }
 
 }  // namespace qlora

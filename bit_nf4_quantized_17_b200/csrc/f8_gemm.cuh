@@ -1,0 +1,78 @@
+// Pieces shared by the 8-bit product kernels (f8_gemm.cu, f8_gemm2.cu).
+#pragma once
+
+#include "f8.cuh"
+#include "tc_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace qlora {
+namespace f8 {
+
+constexpr long long kTimeoutCycles = 4000000000ll;  // ~2 s at 1.9 GHz
+
+struct GemmArgs {
+  int32_t m, n;                // rows (tokens) and columns of C
+  int32_t kb_total, kb_per;    // 128-deep blocks, blocks per split
+  int32_t n_tiles;             // tiles along the P x Q grid's fast axis
+  int32_t stages;
+  int32_t b_mn;                // B MN-major: its contraction axis is its rows
+  int32_t ext_tiles, ext_half, ext_last_steps, ext_mn;
+  int32_t c_f32;
+  const float* sa;             // A's scales, [kb][m]
+  const float* sb;             // B's scales: block column nb at sb[nb * sb_n + kb * sb_k]
+  int64_t sb_n, sb_k;
+  void* c;
+  int64_t c_ld;
+  uint32_t idesc, idesc_ext;
+};
+
+// N consecutive columns of a row of C from column c0 (N = 4 or 16)
+template <int N>
+static __device__ __forceinline__ void store_run(const GemmArgs& p, int64_t row, int64_t c0,
+                                          const float* v) {
+  if (row >= p.m || c0 >= p.n) return;
+  const int64_t at = row * p.c_ld + c0;
+  const bool whole = c0 + N <= p.n;
+  if (p.c_f32) {
+    float* o = static_cast<float*>(p.c) + at;
+    if (whole && (p.c_ld & 3) == 0) {
+#pragma unroll
+      for (int j = 0; j < N; j += 4)
+        *reinterpret_cast<float4*>(o + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (c0 + j < p.n) o[j] = v[j];
+    }
+  } else {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.c) + at;
+    if (whole && N == 16 && (p.c_ld & 7) == 0) {
+      uint32_t w[N / 2];
+#pragma unroll
+      for (int j = 0; j < N / 2; ++j) w[j] = tc::pack_bf16x2(v[2 * j], v[2 * j + 1]);
+#pragma unroll
+      for (int j = 0; j < N / 8; ++j)
+        reinterpret_cast<uint4*>(o)[j] =
+            make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    } else if (whole && N == 4 && (p.c_ld & 3) == 0) {
+      *reinterpret_cast<uint2*>(o) =
+          make_uint2(tc::pack_bf16x2(v[0], v[1]), tc::pack_bf16x2(v[2], v[3]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j)
+        if (c0 + j < p.n) o[j] = __float2bfloat16_rn(v[j]);
+    }
+  }
+}
+
+// The fields of the arguments that do not depend on the kernel.
+GemmArgs gemm_args(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,
+                   const F8Lora& l);
+
+}  // namespace f8
+
+// f8_gemm2.cu: the product on CTA pairs, for sizes whose 256 x 256 tiles fill the GPU.
+qlora_status f8_gemm_pairs(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,
+                           const F8Lora& lora, cudaStream_t s);
+
+}  // namespace qlora

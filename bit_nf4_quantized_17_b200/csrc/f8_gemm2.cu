@@ -1,0 +1,315 @@
+// Matrix product in 8-bit floating point with a scale for each block of 128, on
+// CTA pairs: the large form of f8_gemm.cu (same product, same LoRA term).
+//
+// A cluster of two CTAs computes 256 x 256 tiles of C with pair MMAs
+// (tcgen05.mma.cta_group::2, M = 256, N = 256, issued by the even CTA): each
+// CTA holds its 128 rows of A and half of the B tile, and its TMEM receives its
+// 128 x 256 sums.  A 128-deep block is 512 cycles of MMA; it goes into one of two
+// TMEM accumulators (all 512 columns), and eight warps add the finished one,
+// times its scales, to 128 fp32 sums per thread: 128 multiply-adds and TMEM words
+// per thread and block, about half the MMA's time, so the tensor cores stay fed.
+// A warp's 128 columns lie in one scale block of B, so a thread needs one scale
+// per block.
+//
+// The kernel is persistent: a pair takes tiles pair, pair + pairs, ..., and
+// while its epilogue warps store a tile the next tile's first two blocks run.
+// Tiles go down 16 row tiles before the next column tile, so that the pairs at
+// work share a few columns of B and rows of A that stay in L2.
+//
+// Roles per CTA (320 threads): warp 0 TMA producer, warp 1 TMEM and, in the
+// even CTA, the MMA issuer, warps 2-9 the sums.  TMA loads of both CTAs count on the
+// even CTA's barriers (no multicast).  Every wait is bounded; a CTA whose wait
+// gives up writes NaN to what it had not finished.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "f8_gemm.cuh"
+
+namespace qlora {
+namespace {
+
+using f8::GemmArgs;
+using f8::kTimeoutCycles;
+using f8::store_run;
+
+constexpr int kEpi = 8;
+constexpr int kThreads = 64 + 32 * kEpi;
+constexpr int kStages = 6;
+constexpr int kOpBytes = 16384;              // 128 rows x 128 bytes: A, and this CTA's half of B
+constexpr int kStageBytes = 2 * kOpBytes;
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 256;
+constexpr int kGroup = 16;                   // row tiles per column tile before the next one
+
+__device__ __forceinline__ void tile_at(const GemmArgs& p, int m_tiles, int t, int* mt, int* nt) {
+  const int per = kGroup * p.n_tiles;
+  const int g = t / per, in = t - g * per;
+  const int rows = min(kGroup, m_tiles - g * kGroup);
+  *nt = in / rows;
+  *mt = g * kGroup + in - *nt * rows;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const __grid_constant__ CUtensorMap tmL, const __grid_constant__ CUtensorMap tmR,
+               const GemmArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);  // even CTA's count
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
+  uint64_t* acc_empty = acc_full + 2;  // even CTA's: both CTAs' warps
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int m_tiles = (p.m + 255) / 256;
+  const int tiles = m_tiles * p.n_tiles;
+  const int kn = p.kb_total, total = kn + p.ext_tiles;
+  const int bufs_used = kn + (p.ext_tiles ? 1 : 0);  // accumulators drained per tile
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&full[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&acc_full[b], 1);
+      ptx::mbar_init(&acc_empty[b], 2 * kEpi);
+    }
+    ptx::mbar_init(drain, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmA);
+    ptx::prefetch_tmap(&tmB);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(tmem_slot, 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  // both CTAs' barriers exist before either CTA signals the other's
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0 && lane == 0) {
+    // ------------------------------------------------------ TMA producer
+    int it = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      int mt, nt;
+      tile_at(p, m_tiles, t, &mt, &nt);
+      const int m0 = mt * 256 + static_cast<int>(rank) * 128;
+      const int n0 = nt * 256 + static_cast<int>(rank) * 128;  // this CTA's half of B
+      for (int i = 0; i < total; ++i, ++it) {
+        const int s = it % kStages;
+        ok = ptx::mbar_wait_cluster(&empty[s], ((it / kStages) & 1) ^ 1, kTimeoutCycles,
+                                    abort_flag);
+        if (!ok) break;
+        uint8_t* sa = smem + s * kStageBytes;
+        uint8_t* sb = sa + kOpBytes;
+        const uint32_t bar = ptx::cluster_addr(&full[s], 0);
+        if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+        if (i < kn) {
+          ptx::tma_load_2d_pair(&tmA, bar, sa, i * 128, m0);
+          if (p.b_mn)
+            ptx::tma_load_2d_pair(&tmB, bar, sb, n0, i * 128);
+          else
+            ptx::tma_load_2d_pair(&tmB, bar, sb, i * 128, n0);
+        } else {
+          const int x = i - kn;
+          const int kl = x * 64, kr = (x % p.ext_half) * 64;
+          ptx::tma_load_2d_pair(&tmL, bar, sa, kl, m0);
+          if (p.ext_mn) {
+            ptx::tma_load_2d_pair(&tmR, bar, sb, n0, kr);
+            ptx::tma_load_2d_pair(&tmR, bar, sb + 8192, n0 + 64, kr);
+          } else {
+            ptx::tma_load_2d_pair(&tmR, bar, sb, kr, n0);
+          }
+        }
+      }
+    }
+    // never leave with copies in flight: they all count on the even CTA's barriers
+    if (rank == 0)
+      for (int i = (it > kStages ? it - kStages : 0); i < it; ++i)
+        ptx::mbar_wait_cluster(&full[i % kStages], (i / kStages) & 1, kTimeoutCycles, nullptr);
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ------------------------------------------------------ MMA issuer (even CTA)
+    const uint64_t b_step = p.b_mn ? (4096 >> 4) : (32 >> 4);
+    const uint64_t r_step = p.ext_mn ? (2048 >> 4) : (32 >> 4);
+    int it = 0, use = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      for (int i = 0; i < total; ++i, ++it) {
+        const int s = it % kStages;
+        const int x = i - kn;            // LoRA stage, when >= 0
+        if (x <= 0) {
+          // the first MMA into an accumulator: its previous sums have been read
+          ok = ptx::mbar_wait_cluster(&acc_empty[use & 1], ((use >> 1) & 1) ^ 1, kTimeoutCycles,
+                                      abort_flag);
+          if (!ok) break;
+        }
+        ok = ptx::mbar_wait_cluster(&full[s], (it / kStages) & 1, kTimeoutCycles, abort_flag);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t a_addr = ptx::smem_u32(smem + s * kStageBytes);
+        const uint32_t b_addr = a_addr + kOpBytes;
+        const uint32_t d = tmem + (use & 1) * 256;
+        const uint64_t ad = ptx::sw128_desc(a_addr, 16, 1024);
+        if (x < 0) {
+          const uint64_t bd = ptx::sw128_desc(b_addr, p.b_mn ? kOpBytes : 16, 1024);
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            ptx::umma_f8_pair(d, ad + ((32 * ks) >> 4), bd + b_step * ks, p.idesc, ks ? 1u : 0u);
+        } else {
+          const uint64_t bd = ptx::sw128_desc(b_addr, p.ext_mn ? 8192 : 16, 1024);
+          const int steps = (x % p.ext_half) == p.ext_half - 1 ? p.ext_last_steps : 4;
+          for (int ks = 0; ks < steps; ++ks)
+            ptx::umma_bf16_pair(d, ad + ((32 * ks) >> 4), bd + r_step * ks, p.idesc_ext,
+                                (x | ks) != 0 ? 1u : 0u);
+        }
+        ptx::umma_commit_pair(&empty[s]);
+        if (x < 0 || i == total - 1) {
+          ptx::umma_commit_pair(&acc_full[use & 1]);
+          ++use;
+        }
+      }
+    }
+    // what was issued is done before shared memory and TMEM go
+    ptx::umma_commit_pair(drain);
+    ptx::mbar_wait_cluster(drain, 0, kTimeoutCycles, nullptr);
+  } else if (warp >= 2) {
+    // ------------------------------------------------------ sums
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
+    const uint32_t leader_empty = ptx::cluster_addr(&acc_empty[0], 0);
+    int use = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles; t += pairs) {
+      int mt, nt;
+      tile_at(p, m_tiles, t, &mt, &nt);
+      const int row = mt * 256 + static_cast<int>(rank) * 128 + 32 * quarter + lane;
+      const int col = nt * 256 + 128 * half;
+      const float* sb = p.sb + static_cast<int64_t>(min(col, p.n - 1) >> 7) * p.sb_n;
+      const float* sa = p.sa + row;
+      const bool row_in = row < p.m;
+      auto scale_of = [&](int i) -> float {
+        if (i >= kn) return 1.0f;  // the LoRA term
+        return row_in ? __ldg(sa + static_cast<int64_t>(i) * p.m) * __ldg(sb + i * p.sb_k) : 0.0f;
+      };
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+      constexpr int kAhead = 4;  // blocks whose scales are on their way
+      float sv[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) sv[u] = scale_of(u);
+      for (int i0 = 0; i0 < bufs_used && ok; i0 += kAhead) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+          const int i = i0 + u;
+          if (i < bufs_used && ok) {
+            const int b = use & 1;
+            ok = ptx::mbar_wait_cluster(&acc_full[b], (use >> 1) & 1, kTimeoutCycles, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            ++use;
+            if (ok) {
+              ptx::tc_fence_after();
+              const uint32_t at = tmem + lane_base + b * 256 + half * 128;
+              const float s = sv[u];
+              uint32_t r[2][16];
+              ptx::tmem_ld_x16(at, r[0]);
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                ptx::tmem_ld_wait(r[c & 1]);
+                if (c < 7) ptx::tmem_ld_x16(at + 16 * (c + 1), r[(c + 1) & 1]);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  acc[16 * c + j] = fmaf(__uint_as_float(r[c & 1][j]), s, acc[16 * c + j]);
+              }
+              ptx::tc_fence_before();
+              __syncwarp();
+              if (lane == 0) ptx::mbar_arrive_cluster(leader_empty + 8u * b);
+              sv[u] = scale_of(i + kAhead);
+            }
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+      if (!ok) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) acc[j] = __int_as_float(0x7fffffff);
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) store_run<16>(p, row, col + 16 * c, acc + 16 * c);
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  // neither CTA leaves (or frees TMEM) while the pair may still touch it
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+}  // namespace
+
+qlora_status f8_gemm_pairs(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,
+                           const F8Lora& l, cudaStream_t s) {
+  GemmArgs p = f8::gemm_args(a, b, trans_b, c, c_f32, l);
+  const int64_t m = p.m, n = p.n;
+  CUtensorMap ma, mb, ml, mr;
+  bool ok = make_map(&ma, a.codes, false, a.cols, m, a.ld, 128, 128, true) &&
+            (trans_b ? make_map(&mb, b.codes, false, b.cols, n, b.ld, 128, 128, true)
+                     : make_map(&mb, b.codes, false, n, b.rows, b.ld, 128, 128, true));
+  if (l.r > 0) {
+    const int64_t ld = 2 * lora_span(l.r);
+    ok = ok && make_map(&ml, l.L, true, ld, m, ld, 64, 128, true) &&
+         (p.ext_mn ? make_map(&mr, l.R, true, n, l.r, n, 64, 64, true)
+                   : make_map(&mr, l.R, true, l.r, n, l.r, 64, 128, true));
+  } else {
+    ml = ma;
+    mr = mb;
+  }
+  if (!ok) return QLORA_ERR_CUDA;
+  const int fa = a.format == QLORA_E5M2 ? 1 : 0, fb = b.format == QLORA_E5M2 ? 1 : 0;
+  p.idesc = ptx::idesc_f8(fa, fb, 256, 256, 0, p.b_mn);
+  p.idesc_ext = ptx::idesc_bf16(256, 256, 0, p.ext_mn);
+  p.n_tiles = static_cast<int32_t>(ceil_div(n, 256));
+  const int64_t tiles = ceil_div(m, 256) * p.n_tiles;
+  if (tiles > 0x3fffffff) return QLORA_ERR_SHAPE;
+  const qlora_status cs = ensure_smem(reinterpret_cast<const void*>(f8_pair_kernel), kSmemBytes);
+  if (cs != QLORA_OK) return cs;
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    (void)cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(tiles, sms / 2));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, f8_pair_kernel, ma, mb, ml, mr, p);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return QLORA_ERR_CUDA;
+  }
+  return after_launch("f8_gemm_pairs", s);
+}
+
+}  // namespace qlora

@@ -102,7 +102,9 @@ def _check_product(a, b, trans, out):
 SHAPES = [(1, 16, 16), (1, 128, 128), (1, 1000, 4096), (5, 4104, 1111), (16, 256, 1408),
           (17, 130, 129), (31, 640, 2048), (33, 384, 300), (64, 1000, 2560), (65, 128, 64),
           (128, 128, 1024), (130, 257, 700), (300, 1001, 1111), (512, 512, 8192),
-          (1000, 136, 264)]
+          (1000, 136, 264),
+          # more 128 x 128 tiles than SMs: CTA pairs, more than one tile a pair, ragged edges
+          (2000, 2600, 640), (1500, 1701, 1111), (4300, 4104, 392), (6000, 1030, 100)]
 
 
 @pytest.mark.parametrize("m,n,k", SHAPES)

@@ -116,7 +116,8 @@ def test_kept_input_with_adapters_and_dropout(M):
 
 LIN = [(1, 64, 64, 8), (2, 200, 328, 16), (7, 4096, 1032, 16), (16, 256, 1408, 64),
        (17, 136, 128, 24), (40, 648, 2048, 64), (64, 1000, 264, 8), (65, 128, 64, 16),
-       (130, 256, 704, 40), (300, 1000, 1112, 64), (700, 512, 1024, 136), (520, 1032, 904, 256)]
+       (130, 256, 704, 40), (300, 1000, 1112, 64), (700, 512, 1024, 136), (520, 1032, 904, 256),
+       (1900, 1608, 1704, 72), (2100, 1504, 1800, 256)]
 
 
 @pytest.mark.parametrize("M,N,K,r", LIN)
