@@ -15,16 +15,15 @@
 //   * SWAP, for few tokens: P = B, Q = A (BN = 16, 32, 64): the 128 rows of the
 //     MMA are output columns, no MMA row is wasted on tokens that do not exist,
 //     and B, whose bytes bound the product, is read once.  A thread holds one
-//     output column and all BN tokens; the tokens' scales live one per lane and
-//     are passed round by shuffles.
+//     output column and all BN tokens.
 // B is read in place in both directions of the layer: K-major (C = A B^T) or
 // MN-major (C = A B).
 // Where the tiles would leave SMs idle the contraction is split over the CTAs
 // of a cluster (up to 8) and the fp32 partial tiles are summed in distributed
 // shared memory in split order (deterministic).
 //
-// Roles: warp 0 TMA producer, warp 1 TMEM owner and MMA issuer, the other 4 or
-// 8 warps drain the accumulators.  Every wait is bounded; the call has no
+// Roles: warp 0 TMA producer, warp 1 TMEM owner and MMA issuer, warp 2 the
+// scales, the 4 or 8 warps from warp 4 on drain the accumulators.  Every wait is bounded; the call has no
 // status word, so a CTA whose wait gives up writes NaN to its part.
 #include <cudaTypedefs.h>
 
@@ -53,10 +52,11 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 template <int BN, bool SWAP>
 struct Cfg {
   static constexpr int kEpi = BN >= 128 ? 8 : 4;  // epilogue warps
-  static constexpr int kThreads = 64 + 32 * kEpi;
+  static constexpr int kThreads = 128 + 32 * kEpi;  // TMA, MMA, scales, one idle; the sums
   static constexpr int kCols = BN / (kEpi / 4);   // accumulator columns per thread
   static constexpr int kBufs = BN >= 128 ? 2 : 4; // TMEM accumulators in flight
   static constexpr int kTmem = BN * kBufs;        // 64, 128 or 256 columns
+  using Ring = f8::ScaleRing<SWAP ? BN : 128, 1>;
   static constexpr int kQBytes = BN * 128;
   static constexpr int kStage = kPBytes + kQBytes;
   // fp32 partial tile: rows of tokens, padded against bank conflicts
@@ -76,11 +76,14 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
   // [stages x (P | Q)], reused as the fp32 partial tile once every MMA is done
   const int area = max(p.stages * C::kStage, C::kRedBytes);
   float* red = reinterpret_cast<float*>(smem);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + area);
+  auto* ring = reinterpret_cast<typename C::Ring*>(smem + area);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + 1);
   uint64_t* empty = full + kMaxStages;
   uint64_t* acc_full = empty + kMaxStages;
   uint64_t* acc_empty = acc_full + C::kBufs;
-  uint64_t* drain = acc_empty + C::kBufs;
+  uint64_t* sc_full = acc_empty + C::kBufs;
+  uint64_t* sc_empty = sc_full + 2;
+  uint64_t* drain = sc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -94,7 +97,6 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
   const int kn = max(0, min(p.kb_per, p.kb_total - kb0));
   // the LoRA stages belong to the last split
   const int ext = (z == S - 1) ? p.ext_tiles : 0;
-  const int total = kn + ext;
   const int bufs_used = kn + (ext ? 1 : 0);  // accumulators drained, in order
   const bool p_mn = SWAP && p.b_mn, q_mn = !SWAP && p.b_mn;
   const bool p2_mn = SWAP && p.ext_mn, q2_mn = !SWAP && p.ext_mn;
@@ -107,6 +109,10 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
     for (int b = 0; b < C::kBufs; ++b) {
       ptx::mbar_init(&acc_full[b], 1);
       ptx::mbar_init(&acc_empty[b], C::kEpi);
+    }
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(&sc_full[b], 32);
+      ptx::mbar_init(&sc_empty[b], C::kEpi);
     }
     ptx::mbar_init(drain, 1);
     *abort_flag = 0;
@@ -128,156 +134,194 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
   for (int j = 0; j < C::kCols; ++j) acc[j] = 0.0f;
   // TMEM lanes of a warp are those of its number mod 4
   const int quarter = warp & 3;
-  const int half = (warp - 2) >> 2;  // column half of an 8-warp epilogue
+  const int half = (warp - 4) >> 2;  // column half of an 8-warp epilogue
   bool ok = true;
 
+  // One thread issues all copies and one all MMAs: their loops step the stage, its
+  // phase and the descriptors with adds only.  (Dividing by the runtime stage count
+  // in them cost 600 and 1100 cycles a block, more than the block's bytes or MMAs.)
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------ TMA producer
-    int issued = 0;
-    for (int i = 0; i < total; ++i) {
-      const int s = i % p.stages;
-      if (!ptx::mbar_wait(&empty[s], ((i / p.stages) & 1) ^ 1, kTimeoutCycles, abort_flag)) break;
-      uint8_t* sp = smem + s * C::kStage;
+    int s = 0, issued = 0;
+    uint32_t ph = 1;
+    bool go = true;
+    uint8_t* sp = smem;
+    auto next = [&]() {
+      ++issued;
+      sp += C::kStage;
+      if (++s == p.stages) {
+        s = 0;
+        ph ^= 1;
+        sp = smem;
+      }
+    };
+    for (int i = 0, k = kb0 * 128; i < kn; ++i, k += 128) {
+      go = ptx::mbar_wait(&empty[s], ph, kTimeoutCycles, abort_flag);
+      if (!go) break;
+      ptx::mbar_arrive_expect_tx(&full[s], C::kStage);
+      if (p_mn)
+        ptx::tma_load_2d(&tmP, &full[s], sp, p0, k);
+      else
+        ptx::tma_load_2d(&tmP, &full[s], sp, k, p0);
+      if (q_mn)
+        ptx::tma_load_2d(&tmQ, &full[s], sp + kPBytes, q0, k);
+      else
+        ptx::tma_load_2d(&tmQ, &full[s], sp + kPBytes, k, q0);
+      next();
+    }
+    for (int t = 0, h = 0; t < ext && go; ++t) {
+      go = ptx::mbar_wait(&empty[s], ph, kTimeoutCycles, abort_flag);
+      if (!go) break;
       uint8_t* sq = sp + kPBytes;
       ptx::mbar_arrive_expect_tx(&full[s], C::kStage);
-      if (i < kn) {
-        const int k = (kb0 + i) * 128;
-        if (p_mn)
-          ptx::tma_load_2d(&tmP, &full[s], sp, p0, k);
-        else
-          ptx::tma_load_2d(&tmP, &full[s], sp, k, p0);
-        if (q_mn)
-          ptx::tma_load_2d(&tmQ, &full[s], sq, q0, k);
-        else
-          ptx::tma_load_2d(&tmQ, &full[s], sq, k, q0);
-      } else {
-        // L columns [64 t, 64 t + 64) of [hi | lo], R at ranks 64 (t mod half)
-        const int t = i - kn;
-        const int kl = t * 64, kr = (t % p.ext_half) * 64;
-        if (SWAP) {
-          if (p2_mn) {
-            ptx::tma_load_2d(&tmP2, &full[s], sp, p0, kr);
-            ptx::tma_load_2d(&tmP2, &full[s], sp + 8192, p0 + 64, kr);
-          } else {
-            ptx::tma_load_2d(&tmP2, &full[s], sp, kr, p0);
-          }
-          ptx::tma_load_2d(&tmQ2, &full[s], sq, kl, q0);
+      // L columns [64 t, 64 t + 64) of [hi | lo], R at ranks 64 (t mod half)
+      const int kl = t * 64, kr = h * 64;
+      if (++h == p.ext_half) h = 0;
+      if (SWAP) {
+        if (p2_mn) {
+          ptx::tma_load_2d(&tmP2, &full[s], sp, p0, kr);
+          ptx::tma_load_2d(&tmP2, &full[s], sp + 8192, p0 + 64, kr);
         } else {
-          ptx::tma_load_2d(&tmP2, &full[s], sp, kl, p0);
-          if (q2_mn) {
+          ptx::tma_load_2d(&tmP2, &full[s], sp, kr, p0);
+        }
+        ptx::tma_load_2d(&tmQ2, &full[s], sq, kl, q0);
+      } else {
+        ptx::tma_load_2d(&tmP2, &full[s], sp, kl, p0);
+        if (q2_mn) {
 #pragma unroll
-            for (int h = 0; h < (BN + 63) / 64; ++h)
-              ptx::tma_load_2d(&tmQ2, &full[s], sq + 8192 * h, q0 + 64 * h, kr);
-          } else {
-            ptx::tma_load_2d(&tmQ2, &full[s], sq, kr, q0);
-          }
+          for (int j = 0; j < (BN + 63) / 64; ++j)
+            ptx::tma_load_2d(&tmQ2, &full[s], sq + 8192 * j, q0 + 64 * j, kr);
+        } else {
+          ptx::tma_load_2d(&tmQ2, &full[s], sq, kr, q0);
         }
       }
-      ++issued;
+      next();
     }
     // never leave with copies in flight into this CTA's shared memory
     for (int i = (issued > p.stages ? issued - p.stages : 0); i < issued; ++i)
       ptx::mbar_wait(&full[i % p.stages], (i / p.stages) & 1, kTimeoutCycles, nullptr);
   } else if (warp == 1 && lane == 0) {
     // ------------------------------------------------------ MMA issuer
-    int i = 0;
-    for (; i < total; ++i) {
-      const int s = i % p.stages;
-      const int t = i - kn;             // LoRA stage, when >= 0
-      const int u = t > 0 ? kn : i;     // accumulator use: all LoRA stages share one
-      const int b = u % C::kBufs;
-      if (t <= 0 && !ptx::mbar_wait(&acc_empty[b], ((u / C::kBufs) & 1) ^ 1, kTimeoutCycles,
-                                    abort_flag))
-        break;
-      if (!ptx::mbar_wait(&full[s], (i / p.stages) & 1, kTimeoutCycles, abort_flag)) break;
-      ptx::tc_fence_after();
-      const uint32_t p_addr = ptx::smem_u32(smem + s * C::kStage);
-      const uint32_t q_addr = p_addr + kPBytes;
-      const uint32_t d = tmem + b * BN;
-      if (t < 0) {
-        // MN-major 8-bit tiles: 128 contraction rows of 128 bytes, 32 rows a step
-        const uint64_t pd = ptx::sw128_desc(p_addr, p_mn ? kPBytes : 16, 1024);
-        const uint64_t qd = ptx::sw128_desc(q_addr, q_mn ? kPBytes : 16, 1024);
-        const uint64_t ps = p_mn ? (4096 >> 4) : (32 >> 4);
-        const uint64_t qs = q_mn ? (4096 >> 4) : (32 >> 4);
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          ptx::umma_f8(d, pd + ps * ks, qd + qs * ks, p.idesc, ks ? 1u : 0u);
-      } else {
-        const uint64_t pd = ptx::sw128_desc(p_addr, p2_mn ? 8192 : 16, 1024);
-        const uint64_t qd = ptx::sw128_desc(q_addr, q2_mn ? 8192 : 16, 1024);
-        const uint64_t ps = p2_mn ? (2048 >> 4) : (32 >> 4);
-        const uint64_t qs = q2_mn ? (2048 >> 4) : (32 >> 4);
-        const int steps = (t % p.ext_half) == p.ext_half - 1 ? p.ext_last_steps : 4;
-        for (int ks = 0; ks < steps; ++ks)
-          ptx::umma_bf16(d, pd + ps * ks, qd + qs * ks, p.idesc_ext, (t | ks) != 0 ? 1u : 0u);
+    int s = 0, b = 0;
+    uint32_t ph = 0, bph = 1;
+    bool go = true;
+    // descriptors of stage 0; a stage further is kStage / 16 more (see gemm_tc2.cu)
+    const uint32_t p_addr = ptx::smem_u32(smem), q_addr = p_addr + kPBytes;
+    // MN-major 8-bit tiles: 128 contraction rows of 128 bytes, 32 rows a step
+    const uint64_t pd0 = ptx::sw128_desc(p_addr, p_mn ? kPBytes : 16, 1024);
+    const uint64_t qd0 = ptx::sw128_desc(q_addr, q_mn ? kPBytes : 16, 1024);
+    const uint64_t ps = p_mn ? (4096 >> 4) : (32 >> 4), qs = q_mn ? (4096 >> 4) : (32 >> 4);
+    const uint32_t idesc = p.idesc;
+    uint64_t off = 0;
+    auto next = [&]() {
+      off += C::kStage >> 4;
+      if (++s == p.stages) {
+        s = 0;
+        ph ^= 1;
+        off = 0;
       }
+    };
+    for (int i = 0; i < kn; ++i) {
+      go = ptx::mbar_wait(&acc_empty[b], bph, kTimeoutCycles, abort_flag) &&
+           ptx::mbar_wait(&full[s], ph, kTimeoutCycles, abort_flag);
+      if (!go) break;
+      ptx::tc_fence_after();
+      const uint32_t d = tmem + b * BN;
+      const uint64_t pd = pd0 + off, qd = qd0 + off;
+      ptx::umma_f8(d, pd, qd, idesc, 0u);
+      ptx::umma_f8(d, pd + ps, qd + qs, idesc, 1u);
+      ptx::umma_f8(d, pd + 2 * ps, qd + 2 * qs, idesc, 1u);
+      ptx::umma_f8(d, pd + 3 * ps, qd + 3 * qs, idesc, 1u);
       ptx::umma_commit(&empty[s]);
-      if (t < 0 || i == total - 1) ptx::umma_commit(&acc_full[b]);
+      ptx::umma_commit(&acc_full[b]);
+      next();
+      if (++b == C::kBufs) {
+        b = 0;
+        bph ^= 1;
+      }
     }
-    if (i < total) {
+    if (ext && go) {
+      // every LoRA stage goes into one accumulator
+      go = ptx::mbar_wait(&acc_empty[b], bph, kTimeoutCycles, abort_flag);
+      const uint64_t p2d = ptx::sw128_desc(p_addr, p2_mn ? 8192 : 16, 1024);
+      const uint64_t q2d = ptx::sw128_desc(q_addr, q2_mn ? 8192 : 16, 1024);
+      const uint64_t p2s = p2_mn ? (2048 >> 4) : (32 >> 4), q2s = q2_mn ? (2048 >> 4) : (32 >> 4);
+      for (int t = 0, h = 0; t < ext && go; ++t) {
+        go = ptx::mbar_wait(&full[s], ph, kTimeoutCycles, abort_flag);
+        if (!go) break;
+        ptx::tc_fence_after();
+        const int steps = ++h == p.ext_half ? p.ext_last_steps : 4;
+        if (h == p.ext_half) h = 0;
+        for (int ks = 0; ks < steps; ++ks)
+          ptx::umma_bf16(tmem + b * BN, p2d + off + p2s * ks, q2d + off + q2s * ks, p.idesc_ext,
+                         (t | ks) != 0 ? 1u : 0u);
+        ptx::umma_commit(&empty[s]);
+        next();
+      }
+      if (go) ptx::umma_commit(&acc_full[b]);
+    }
+    if (!go) {
       // gave up: what was issued is done before shared memory and TMEM go
       ptx::umma_commit(drain);
       ptx::mbar_wait(drain, 0, kTimeoutCycles, nullptr);
     }
-  } else if (warp >= 2) {
+  } else if (warp == 2) {
+    // ------------------------------------------------------ scales
+    for (int kb = 0, c = 0; kb < kn; kb += f8::kChunk, ++c) {
+      bool go = ptx::mbar_wait(&sc_empty[c & 1], ((c >> 1) & 1) ^ 1, kTimeoutCycles, abort_flag);
+      go = __all_sync(0xffffffffu, go);
+      if (!go) break;
+      f8::fill_scales(p, ring, c & 1, kb0 + kb, kb0 + kn, SWAP ? q0 : p0, (SWAP ? p0 : q0) >> 7,
+                      (p.n + 127) >> 7, lane, &sc_full[c & 1]);
+    }
+    f8::cp_async_wait_all();
+  } else if (warp >= 4) {
     // ------------------------------------------------------ epilogue warps
     const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
     const int row = 32 * quarter + lane;  // row of the P tile
-    // scales of block i of this split: SWAP keeps token q0 + lane (+ 32) per
-    // lane, otherwise the thread's own row; times B's scale of the tile
-    constexpr int kSc = SWAP ? (BN + 31) / 32 : 1;
-    const float* sb = p.sb + static_cast<int64_t>((SWAP ? p0 : q0) >> 7) * p.sb_n;
-    auto scale_of = [&](int i, float (&sv)[kSc]) {
-      if (i >= kn) return;
-      const int64_t kb = kb0 + i;
-      const float w = __ldg(sb + kb * p.sb_k);
+    int chunk = 0;
+    for (int i = 0; i < bufs_used; ++i) {
+      const int b = i % C::kBufs, in = i % f8::kChunk;  // (both powers of two)
+      const bool lora = i == kn;
+      if (!lora && in == 0)
+        ok = ptx::mbar_wait(&sc_full[chunk & 1], (chunk >> 1) & 1, kTimeoutCycles, abort_flag);
+      ok = ok && ptx::mbar_wait(&acc_full[b], (i / C::kBufs) & 1, kTimeoutCycles, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      ptx::tc_fence_after();
+      const float* sa = ring->a[chunk & 1][in];
+      const float sb = lora ? 1.0f : ring->b[chunk & 1][in][0];
+      const float s_row = (SWAP || lora) ? 1.0f : sa[row] * sb;
+      const uint32_t at = tmem + lane_base + b * BN + half * C::kCols;
+      uint32_t r[2][16];
+      ptx::tmem_ld_x16(at, r[0]);
 #pragma unroll
-      for (int h = 0; h < kSc; ++h) {
-        const int tok = SWAP ? q0 + 32 * h + lane : p0 + row;
-        sv[h] = tok < p.m ? __ldg(p.sa + kb * p.m + tok) * w : 0.0f;
-      }
-    };
-    constexpr int kAhead = 4;  // blocks whose scales are on their way
-    float sv[kAhead][kSc];
+      for (int c = 0; c < C::kCols / 16; ++c) {
+        ptx::tmem_ld_wait(r[c & 1]);
+        if (c + 1 < C::kCols / 16) ptx::tmem_ld_x16(at + 16 * (c + 1), r[(c + 1) & 1]);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) scale_of(u, sv[u]);
-    for (int i0 = 0; i0 < bufs_used && ok; i0 += kAhead) {
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int i = i0 + u;
-        if (i < bufs_used && ok) {
-          const int b = i % C::kBufs;
-          ok = ptx::mbar_wait(&acc_full[b], (i / C::kBufs) & 1, kTimeoutCycles, abort_flag);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            ptx::tc_fence_after();
-            const uint32_t at = tmem + lane_base + b * BN + half * C::kCols;
-            const bool lora = i == kn;
-            uint32_t r[2][16];
-            ptx::tmem_ld_x16(at, r[0]);
-#pragma unroll
-            for (int c = 0; c < C::kCols / 16; ++c) {
-              ptx::tmem_ld_wait(r[c & 1]);
-              if (c + 1 < C::kCols / 16) ptx::tmem_ld_x16(at + 16 * (c + 1), r[(c + 1) & 1]);
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                float s;
-                if (SWAP)
-                  s = __shfl_sync(0xffffffffu, sv[u][(16 * c + j) / 32], (16 * c + j) & 31);
-                else
-                  s = sv[u][0];
-                if (lora) s = 1.0f;
-                acc[16 * c + j] = fmaf(__uint_as_float(r[c & 1][j]), s, acc[16 * c + j]);
-              }
-            }
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&acc_empty[b]);
-            scale_of(i + kAhead, sv[u]);
+        for (int j = 0; j < 16; j += 4) {
+          float4 s = make_float4(s_row, s_row, s_row, s_row);
+          if (SWAP && !lora) {
+            s = *reinterpret_cast<const float4*>(sa + 16 * c + j);  // one address for all lanes
+            s.x *= sb;
+            s.y *= sb;
+            s.z *= sb;
+            s.w *= sb;
           }
+          acc[16 * c + j] = fmaf(__uint_as_float(r[c & 1][j]), s.x, acc[16 * c + j]);
+          acc[16 * c + j + 1] = fmaf(__uint_as_float(r[c & 1][j + 1]), s.y, acc[16 * c + j + 1]);
+          acc[16 * c + j + 2] = fmaf(__uint_as_float(r[c & 1][j + 2]), s.z, acc[16 * c + j + 2]);
+          acc[16 * c + j + 3] = fmaf(__uint_as_float(r[c & 1][j + 3]), s.w, acc[16 * c + j + 3]);
         }
       }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        ptx::mbar_arrive(&acc_empty[b]);
+        if (!lora && (in == f8::kChunk - 1 || i == kn - 1)) ptx::mbar_arrive(&sc_empty[chunk & 1]);
+      }
+      if (in == f8::kChunk - 1) ++chunk;
     }
     ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     if (!ok) {
@@ -311,7 +355,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
     // this CTA has read them, and the producer that every copy has landed
     ptx::tc_fence_before();
     __syncthreads();
-    if (warp >= 2) {
+    if (warp >= 4) {
       const int row = 32 * quarter + lane;
       if (SWAP) {
 #pragma unroll
@@ -397,7 +441,8 @@ qlora_status launch(const qlora_f8& a, const qlora_f8& b, bool trans_b, GemmArgs
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p_tiles * q_tiles), 1, static_cast<unsigned>(splits));
   cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = 1024 + std::max(p.stages * C::kStage, C::kRedBytes) + 512;
+  cfg.dynamicSmemBytes =
+      1024 + std::max(p.stages * C::kStage, C::kRedBytes) + sizeof(typename C::Ring) + 512;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

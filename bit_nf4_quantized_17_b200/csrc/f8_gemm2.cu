@@ -16,8 +16,8 @@
 // Tiles go down 16 row tiles before the next column tile, so that the pairs at
 // work share a few columns of B and rows of A that stay in L2.
 //
-// Roles per CTA (320 threads): warp 0 TMA producer, warp 1 TMEM and, in the
-// even CTA, the MMA issuer, warps 2-9 the sums.  TMA loads of both CTAs count on the
+// Roles per CTA (384 threads): warp 0 TMA producer, warp 1 TMEM and, in the
+// even CTA, the MMA issuer, warp 2 the scales, warps 4-11 the sums.  TMA loads of both CTAs count on the
 // even CTA's barriers (no multicast).  Every wait is bounded; a CTA whose wait
 // gives up writes NaN to what it had not finished.
 #include <cudaTypedefs.h>
@@ -34,11 +34,13 @@ using f8::kTimeoutCycles;
 using f8::store_run;
 
 constexpr int kEpi = 8;
-constexpr int kThreads = 64 + 32 * kEpi;
+constexpr int kRoleWarps = 4;                // TMA, MMA, scales, one idle
+constexpr int kThreads = 32 * (kRoleWarps + kEpi);
 constexpr int kStages = 6;
 constexpr int kOpBytes = 16384;              // 128 rows x 128 bytes: A, and this CTA's half of B
 constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 256;
+using Ring = f8::ScaleRing<128, 2>;
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + sizeof(Ring) + 256;
 constexpr int kGroup = 16;                   // row tiles per column tile before the next one
 
 __device__ __forceinline__ void tile_at(const GemmArgs& p, int m_tiles, int t, int* mt, int* nt) {
@@ -56,11 +58,14 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kStages * kStageBytes);  // even CTA's count
+  Ring* ring = reinterpret_cast<Ring*>(smem + kStages * kStageBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + 1);  // even CTA's count
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
   uint64_t* acc_empty = acc_full + 2;  // even CTA's: both CTAs' warps
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* sc_full = acc_empty + 2;
+  uint64_t* sc_empty = sc_full + 2;
+  uint64_t* drain = sc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -69,7 +74,7 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int m_tiles = (p.m + 255) / 256;
   const int tiles = m_tiles * p.n_tiles;
-  const int kn = p.kb_total, total = kn + p.ext_tiles;
+  const int kn = p.kb_total;
   const int bufs_used = kn + (p.ext_tiles ? 1 : 0);  // accumulators drained per tile
 
   if (threadIdx.x == 0) {
@@ -80,6 +85,8 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&acc_full[b], 1);
       ptx::mbar_init(&acc_empty[b], 2 * kEpi);
+      ptx::mbar_init(&sc_full[b], 32);
+      ptx::mbar_init(&sc_empty[b], kEpi);
     }
     ptx::mbar_init(drain, 1);
     *abort_flag = 0;
@@ -97,41 +104,56 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
+  // (The loops of the two issuing threads step the stage, its phase and the
+  // descriptors with adds only: see f8_gemm.cu.)
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------ TMA producer
-    int it = 0;
+    int it = 0, s = 0;
+    uint32_t ph = 1;
     bool ok = true;
+    const uint32_t bar0 = ptx::cluster_addr(&full[0], 0);
+    auto next = [&]() {
+      ++it;
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1;
+      }
+    };
     for (int t = pair; t < tiles && ok; t += pairs) {
       int mt, nt;
       tile_at(p, m_tiles, t, &mt, &nt);
       const int m0 = mt * 256 + static_cast<int>(rank) * 128;
       const int n0 = nt * 256 + static_cast<int>(rank) * 128;  // this CTA's half of B
-      for (int i = 0; i < total; ++i, ++it) {
-        const int s = it % kStages;
-        ok = ptx::mbar_wait_cluster(&empty[s], ((it / kStages) & 1) ^ 1, kTimeoutCycles,
-                                    abort_flag);
+      for (int i = 0, k = 0; i < kn; ++i, k += 128) {
+        ok = ptx::mbar_wait_cluster(&empty[s], ph, kTimeoutCycles, abort_flag);
+        if (!ok) break;
+        uint8_t* sa = smem + s * kStageBytes;
+        const uint32_t bar = bar0 + 8u * s;
+        if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
+        ptx::tma_load_2d_pair(&tmA, bar, sa, k, m0);
+        if (p.b_mn)
+          ptx::tma_load_2d_pair(&tmB, bar, sa + kOpBytes, n0, k);
+        else
+          ptx::tma_load_2d_pair(&tmB, bar, sa + kOpBytes, k, n0);
+        next();
+      }
+      for (int x = 0, h = 0; x < p.ext_tiles && ok; ++x) {
+        ok = ptx::mbar_wait_cluster(&empty[s], ph, kTimeoutCycles, abort_flag);
         if (!ok) break;
         uint8_t* sa = smem + s * kStageBytes;
         uint8_t* sb = sa + kOpBytes;
-        const uint32_t bar = ptx::cluster_addr(&full[s], 0);
+        const uint32_t bar = bar0 + 8u * s;
         if (rank == 0) ptx::mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
-        if (i < kn) {
-          ptx::tma_load_2d_pair(&tmA, bar, sa, i * 128, m0);
-          if (p.b_mn)
-            ptx::tma_load_2d_pair(&tmB, bar, sb, n0, i * 128);
-          else
-            ptx::tma_load_2d_pair(&tmB, bar, sb, i * 128, n0);
+        const int kr = h * 64;
+        if (++h == p.ext_half) h = 0;
+        ptx::tma_load_2d_pair(&tmL, bar, sa, x * 64, m0);
+        if (p.ext_mn) {
+          ptx::tma_load_2d_pair(&tmR, bar, sb, n0, kr);
+          ptx::tma_load_2d_pair(&tmR, bar, sb + 8192, n0 + 64, kr);
         } else {
-          const int x = i - kn;
-          const int kl = x * 64, kr = (x % p.ext_half) * 64;
-          ptx::tma_load_2d_pair(&tmL, bar, sa, kl, m0);
-          if (p.ext_mn) {
-            ptx::tma_load_2d_pair(&tmR, bar, sb, n0, kr);
-            ptx::tma_load_2d_pair(&tmR, bar, sb + 8192, n0 + 64, kr);
-          } else {
-            ptx::tma_load_2d_pair(&tmR, bar, sb, kr, n0);
-          }
+          ptx::tma_load_2d_pair(&tmR, bar, sb, kr, n0);
         }
+        next();
       }
     }
     // never leave with copies in flight: they all count on the even CTA's barriers
@@ -140,113 +162,153 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         ptx::mbar_wait_cluster(&full[i % kStages], (i / kStages) & 1, kTimeoutCycles, nullptr);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ------------------------------------------------------ MMA issuer (even CTA)
-    const uint64_t b_step = p.b_mn ? (4096 >> 4) : (32 >> 4);
-    const uint64_t r_step = p.ext_mn ? (2048 >> 4) : (32 >> 4);
-    int it = 0, use = 0;
+    const uint32_t a_addr = ptx::smem_u32(smem), b_addr = a_addr + kOpBytes;
+    const uint64_t ad0 = ptx::sw128_desc(a_addr, 16, 1024);
+    const uint64_t bd0 = ptx::sw128_desc(b_addr, p.b_mn ? kOpBytes : 16, 1024);
+    const uint64_t rd0 = ptx::sw128_desc(b_addr, p.ext_mn ? 8192 : 16, 1024);
+    const uint64_t bs = p.b_mn ? (4096 >> 4) : (32 >> 4);
+    const uint64_t rs = p.ext_mn ? (2048 >> 4) : (32 >> 4);
+    const uint32_t idesc = p.idesc;
+    int s = 0;
+    uint32_t ph = 0, b = 0, bph = 1;
+    uint64_t off = 0;
     bool ok = true;
+    auto next = [&]() {
+      off += kStageBytes >> 4;
+      if (++s == kStages) {
+        s = 0;
+        ph ^= 1;
+        off = 0;
+      }
+    };
+    auto next_acc = [&]() {
+      b ^= 1;
+      if (b == 0) bph ^= 1;
+    };
     for (int t = pair; t < tiles && ok; t += pairs) {
-      for (int i = 0; i < total; ++i, ++it) {
-        const int s = it % kStages;
-        const int x = i - kn;            // LoRA stage, when >= 0
-        if (x <= 0) {
-          // the first MMA into an accumulator: its previous sums have been read
-          ok = ptx::mbar_wait_cluster(&acc_empty[use & 1], ((use >> 1) & 1) ^ 1, kTimeoutCycles,
-                                      abort_flag);
-          if (!ok) break;
-        }
-        ok = ptx::mbar_wait_cluster(&full[s], (it / kStages) & 1, kTimeoutCycles, abort_flag);
+      for (int i = 0; i < kn; ++i) {
+        ok = ptx::mbar_wait_cluster(&acc_empty[b], bph, kTimeoutCycles, abort_flag) &&
+             ptx::mbar_wait_cluster(&full[s], ph, kTimeoutCycles, abort_flag);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t a_addr = ptx::smem_u32(smem + s * kStageBytes);
-        const uint32_t b_addr = a_addr + kOpBytes;
-        const uint32_t d = tmem + (use & 1) * 256;
-        const uint64_t ad = ptx::sw128_desc(a_addr, 16, 1024);
-        if (x < 0) {
-          const uint64_t bd = ptx::sw128_desc(b_addr, p.b_mn ? kOpBytes : 16, 1024);
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            ptx::umma_f8_pair(d, ad + ((32 * ks) >> 4), bd + b_step * ks, p.idesc, ks ? 1u : 0u);
-        } else {
-          const uint64_t bd = ptx::sw128_desc(b_addr, p.ext_mn ? 8192 : 16, 1024);
-          const int steps = (x % p.ext_half) == p.ext_half - 1 ? p.ext_last_steps : 4;
-          for (int ks = 0; ks < steps; ++ks)
-            ptx::umma_bf16_pair(d, ad + ((32 * ks) >> 4), bd + r_step * ks, p.idesc_ext,
-                                (x | ks) != 0 ? 1u : 0u);
-        }
+        const uint32_t d = tmem + b * 256;
+        const uint64_t ad = ad0 + off, bd = bd0 + off;
+        ptx::umma_f8_pair(d, ad, bd, idesc, 0u);
+        ptx::umma_f8_pair(d, ad + 2, bd + bs, idesc, 1u);
+        ptx::umma_f8_pair(d, ad + 4, bd + 2 * bs, idesc, 1u);
+        ptx::umma_f8_pair(d, ad + 6, bd + 3 * bs, idesc, 1u);
         ptx::umma_commit_pair(&empty[s]);
-        if (x < 0 || i == total - 1) {
-          ptx::umma_commit_pair(&acc_full[use & 1]);
-          ++use;
+        ptx::umma_commit_pair(&acc_full[b]);
+        next();
+        next_acc();
+      }
+      if (p.ext_tiles && ok) {
+        // every LoRA stage goes into one accumulator
+        ok = ptx::mbar_wait_cluster(&acc_empty[b], bph, kTimeoutCycles, abort_flag);
+        for (int x = 0, h = 0; x < p.ext_tiles && ok; ++x) {
+          ok = ptx::mbar_wait_cluster(&full[s], ph, kTimeoutCycles, abort_flag);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const int steps = ++h == p.ext_half ? p.ext_last_steps : 4;
+          if (h == p.ext_half) h = 0;
+          for (int ks = 0; ks < steps; ++ks)
+            ptx::umma_bf16_pair(tmem + b * 256, ad0 + off + 2 * ks, rd0 + off + rs * ks,
+                                p.idesc_ext, (x | ks) != 0 ? 1u : 0u);
+          ptx::umma_commit_pair(&empty[s]);
+          next();
         }
+        if (!ok) break;
+        ptx::umma_commit_pair(&acc_full[b]);
+        next_acc();
       }
     }
     // what was issued is done before shared memory and TMEM go
     ptx::umma_commit_pair(drain);
     ptx::mbar_wait_cluster(drain, 0, kTimeoutCycles, nullptr);
-  } else if (warp >= 2) {
+  } else if (warp == 2) {
+    // ------------------------------------------------------ scales
+    int chunk = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      int mt, nt;
+      tile_at(p, m_tiles, t, &mt, &nt);
+      for (int kb = 0; kb < kn; kb += f8::kChunk, ++chunk) {
+        ok = ptx::mbar_wait(&sc_empty[chunk & 1], ((chunk >> 1) & 1) ^ 1, kTimeoutCycles,
+                            abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        f8::fill_scales(p, ring, chunk & 1, kb, kn, mt * 256 + static_cast<int>(rank) * 128,
+                        2 * nt, (p.n + 127) >> 7, lane, &sc_full[chunk & 1]);
+      }
+    }
+    f8::cp_async_wait_all();
+  } else if (warp >= kRoleWarps) {
     // ------------------------------------------------------ sums
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int quarter = warp & 3, half = (warp - kRoleWarps) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
     const uint32_t leader_empty = ptx::cluster_addr(&acc_empty[0], 0);
-    int use = 0;
+    const int lrow = 32 * quarter + lane;
+    int use = 0, chunk = 0;
     bool ok = true;
     for (int t = pair; t < tiles; t += pairs) {
       int mt, nt;
       tile_at(p, m_tiles, t, &mt, &nt);
-      const int row = mt * 256 + static_cast<int>(rank) * 128 + 32 * quarter + lane;
-      const int col = nt * 256 + 128 * half;
-      const float* sb = p.sb + static_cast<int64_t>(min(col, p.n - 1) >> 7) * p.sb_n;
-      const float* sa = p.sa + row;
-      const bool row_in = row < p.m;
-      auto scale_of = [&](int i) -> float {
-        if (i >= kn) return 1.0f;  // the LoRA term
-        return row_in ? __ldg(sa + static_cast<int64_t>(i) * p.m) * __ldg(sb + i * p.sb_k) : 0.0f;
-      };
-      float acc[128];
+      // two sums a register pair: one instruction multiplies and adds both
+      uint64_t acc[64];
 #pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
-      constexpr int kAhead = 4;  // blocks whose scales are on their way
-      float sv[kAhead];
+      for (int j = 0; j < 64; ++j) acc[j] = 0ull;
+      for (int i = 0; i < bufs_used && ok; ++i, ++use) {
+        const int b = use & 1, in = i % f8::kChunk;
+        float s = 1.0f;  // the LoRA term
+        if (i < kn) {
+          if (in == 0)
+            ok = ptx::mbar_wait(&sc_full[chunk & 1], (chunk >> 1) & 1, kTimeoutCycles, abort_flag);
+          s = ring->a[chunk & 1][in][lrow] * ring->b[chunk & 1][in][half];
+        }
+        ok = ok && ptx::mbar_wait_cluster(&acc_full[b], (use >> 1) & 1, kTimeoutCycles, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t at = tmem + lane_base + b * 256 + half * 128;
+        uint64_t ss;
+        asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+        uint32_t r[2][16];
+        ptx::tmem_ld_x16(at, r[0]);
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) sv[u] = scale_of(u);
-      for (int i0 = 0; i0 < bufs_used && ok; i0 += kAhead) {
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-          const int i = i0 + u;
-          if (i < bufs_used && ok) {
-            const int b = use & 1;
-            ok = ptx::mbar_wait_cluster(&acc_full[b], (use >> 1) & 1, kTimeoutCycles, abort_flag);
-            ok = __all_sync(0xffffffffu, ok);
-            ++use;
-            if (ok) {
-              ptx::tc_fence_after();
-              const uint32_t at = tmem + lane_base + b * 256 + half * 128;
-              const float s = sv[u];
-              uint32_t r[2][16];
-              ptx::tmem_ld_x16(at, r[0]);
-#pragma unroll
-              for (int c = 0; c < 8; ++c) {
-                ptx::tmem_ld_wait(r[c & 1]);
-                if (c < 7) ptx::tmem_ld_x16(at + 16 * (c + 1), r[(c + 1) & 1]);
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  acc[16 * c + j] = fmaf(__uint_as_float(r[c & 1][j]), s, acc[16 * c + j]);
-              }
-              ptx::tc_fence_before();
-              __syncwarp();
-              if (lane == 0) ptx::mbar_arrive_cluster(leader_empty + 8u * b);
-              sv[u] = scale_of(i + kAhead);
-            }
+        for (int c = 0; c < 8; ++c) {
+          ptx::tmem_ld_wait(r[c & 1]);
+          if (c < 7) ptx::tmem_ld_x16(at + 16 * (c + 1), r[(c + 1) & 1]);
+          if (c == 7) {
+            // everything is in registers: the accumulator may be overwritten
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(leader_empty + 8u * b);
           }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint64_t x;
+            asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(r[c & 1][2 * j]), "r"(r[c & 1][2 * j + 1]));
+            asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[8 * c + j]) : "l"(x), "l"(ss));
+          }
+        }
+        if (i < kn && (in == f8::kChunk - 1 || i == kn - 1)) {
+          if (lane == 0) ptx::mbar_arrive(&sc_empty[chunk & 1]);
+          ++chunk;
         }
       }
       ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-      if (!ok) {
+      const int row = mt * 256 + static_cast<int>(rank) * 128 + lrow;
+      const int col = nt * 256 + 128 * half;
 #pragma unroll
-        for (int j = 0; j < 128; ++j) acc[j] = __int_as_float(0x7fffffff);
+      for (int c = 0; c < 8; ++c) {
+        float v[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * j]), "=f"(v[2 * j + 1]) : "l"(acc[8 * c + j]));
+          if (!ok) v[2 * j] = v[2 * j + 1] = __int_as_float(0x7fffffff);
+        }
+        store_run<16>(p, row, col + 16 * c, v);
       }
-#pragma unroll
-      for (int c = 0; c < 8; ++c) store_run<16>(p, row, col + 16 * c, acc + 16 * c);
     }
   }
   ptx::tc_fence_before();
