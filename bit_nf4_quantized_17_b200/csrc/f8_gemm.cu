@@ -87,7 +87,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t S = gridDim.z, z = blockIdx.z;  // the cluster spans z
   // tile of P (128 rows) and of Q (BN rows)
   const int qt = SWAP ? blockIdx.x / p.n_tiles : blockIdx.x % p.n_tiles;
@@ -140,7 +140,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
   // One thread issues all copies and one all MMAs: their loops step the stage, its
   // phase and the descriptors with adds only.  (Dividing by the runtime stage count
   // in them cost 600 and 1100 cycles a block, more than the block's bytes or MMAs.)
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && ptx::elect_one()) {
     // ------------------------------------------------------ TMA producer
     int s = 0, issued = 0;
     uint32_t ph = 1;
@@ -200,7 +200,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
     // never leave with copies in flight into this CTA's shared memory
     for (int i = (issued > p.stages ? issued - p.stages : 0); i < issued; ++i)
       ptx::mbar_wait(&full[i % p.stages], (i / p.stages) & 1, kTimeoutCycles, nullptr);
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1 && ptx::elect_one()) {
     // ------------------------------------------------------ MMA issuer
     int s = 0, b = 0;
     uint32_t ph = 0, bph = 1;

@@ -69,7 +69,7 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int m_tiles = (p.m + 255) / 256;
@@ -106,7 +106,7 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
   // (The loops of the two issuing threads step the stage, its phase and the
   // descriptors with adds only: see f8_gemm.cu.)
-  if (warp == 0 && lane == 0) {
+  if (warp == 0 && ptx::elect_one()) {
     // ------------------------------------------------------ TMA producer
     int it = 0, s = 0;
     uint32_t ph = 1;
@@ -125,7 +125,7 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       const int m0 = mt * 256 + static_cast<int>(rank) * 128;
       const int n0 = nt * 256 + static_cast<int>(rank) * 128;  // this CTA's half of B
       for (int i = 0, k = 0; i < kn; ++i, k += 128) {
-        ok = ptx::mbar_wait_cluster(&empty[s], ph, kTimeoutCycles, abort_flag);
+        ok = ptx::mbar_wait(&empty[s], ph, kTimeoutCycles, abort_flag);
         if (!ok) break;
         uint8_t* sa = smem + s * kStageBytes;
         const uint32_t bar = bar0 + 8u * s;
@@ -138,7 +138,7 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         next();
       }
       for (int x = 0, h = 0; x < p.ext_tiles && ok; ++x) {
-        ok = ptx::mbar_wait_cluster(&empty[s], ph, kTimeoutCycles, abort_flag);
+        ok = ptx::mbar_wait(&empty[s], ph, kTimeoutCycles, abort_flag);
         if (!ok) break;
         uint8_t* sa = smem + s * kStageBytes;
         uint8_t* sb = sa + kOpBytes;
@@ -159,8 +159,8 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     // never leave with copies in flight: they all count on the even CTA's barriers
     if (rank == 0)
       for (int i = (it > kStages ? it - kStages : 0); i < it; ++i)
-        ptx::mbar_wait_cluster(&full[i % kStages], (i / kStages) & 1, kTimeoutCycles, nullptr);
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+        ptx::mbar_wait(&full[i % kStages], (i / kStages) & 1, kTimeoutCycles, nullptr);
+  } else if (warp == 1 && rank == 0 && ptx::elect_one()) {
     // ------------------------------------------------------ MMA issuer (even CTA)
     const uint32_t a_addr = ptx::smem_u32(smem), b_addr = a_addr + kOpBytes;
     const uint64_t ad0 = ptx::sw128_desc(a_addr, 16, 1024);
@@ -187,8 +187,8 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     };
     for (int t = pair; t < tiles && ok; t += pairs) {
       for (int i = 0; i < kn; ++i) {
-        ok = ptx::mbar_wait_cluster(&acc_empty[b], bph, kTimeoutCycles, abort_flag) &&
-             ptx::mbar_wait_cluster(&full[s], ph, kTimeoutCycles, abort_flag);
+        ok = ptx::mbar_wait(&acc_empty[b], bph, kTimeoutCycles, abort_flag) &&
+             ptx::mbar_wait(&full[s], ph, kTimeoutCycles, abort_flag);
         if (!ok) break;
         ptx::tc_fence_after();
         const uint32_t d = tmem + b * 256;
@@ -204,9 +204,9 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       }
       if (p.ext_tiles && ok) {
         // every LoRA stage goes into one accumulator
-        ok = ptx::mbar_wait_cluster(&acc_empty[b], bph, kTimeoutCycles, abort_flag);
+        ok = ptx::mbar_wait(&acc_empty[b], bph, kTimeoutCycles, abort_flag);
         for (int x = 0, h = 0; x < p.ext_tiles && ok; ++x) {
-          ok = ptx::mbar_wait_cluster(&full[s], ph, kTimeoutCycles, abort_flag);
+          ok = ptx::mbar_wait(&full[s], ph, kTimeoutCycles, abort_flag);
           if (!ok) break;
           ptx::tc_fence_after();
           const int steps = ++h == p.ext_half ? p.ext_last_steps : 4;
@@ -224,7 +224,7 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     }
     // what was issued is done before shared memory and TMEM go
     ptx::umma_commit_pair(drain);
-    ptx::mbar_wait_cluster(drain, 0, kTimeoutCycles, nullptr);
+    ptx::mbar_wait(drain, 0, kTimeoutCycles, nullptr);
   } else if (warp == 2) {
     // ------------------------------------------------------ scales
     int chunk = 0;
@@ -265,7 +265,7 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             ok = ptx::mbar_wait(&sc_full[chunk & 1], (chunk >> 1) & 1, kTimeoutCycles, abort_flag);
           s = ring->a[chunk & 1][in][lrow] * ring->b[chunk & 1][in][half];
         }
-        ok = ok && ptx::mbar_wait_cluster(&acc_full[b], (use >> 1) & 1, kTimeoutCycles, abort_flag);
+        ok = ok && ptx::mbar_wait(&acc_full[b], (use >> 1) & 1, kTimeoutCycles, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ptx::tc_fence_after();

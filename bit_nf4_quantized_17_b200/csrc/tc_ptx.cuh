@@ -13,6 +13,19 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// True in exactly one lane of a converged warp.  A branch on it, unlike one on
+// lane == 0, is known to run one thread, so that the operands of the MMA and TMA
+// instructions in it can stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0u;
+}
+
 // ---------------------------------------------------------------- mbarrier
 // Suspend-time hint of the waits (ns): a waiting thread sleeps in the
 // try_wait until the phase completes or this long has passed, instead of
