@@ -51,6 +51,19 @@ __device__ __forceinline__ void tile_at(const GemmArgs& p, int m_tiles, int t, i
   *mt = g * kGroup + in - *nt * rows;
 }
 
+// acc[at ..] += s r, two sums an instruction.
+__device__ __forceinline__ void add64(uint64_t (&acc)[64], int at, const uint32_t (&r)[64],
+                                      float s) {
+  uint64_t ss;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(r[2 * j]), "r"(r[2 * j + 1]));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[at + j]) : "l"(x), "l"(ss));
+  }
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
 f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmL, const __grid_constant__ CUtensorMap tmR,
@@ -62,8 +75,8 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + 1);  // even CTA's count
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
-  uint64_t* acc_empty = acc_full + 2;  // even CTA's: both CTAs' warps
-  uint64_t* sc_full = acc_empty + 2;
+  uint64_t* acc_empty = acc_full + 4;  // even CTA's: both CTAs' warps
+  uint64_t* sc_full = acc_empty + 4;
   uint64_t* sc_empty = sc_full + 2;
   uint64_t* drain = sc_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -75,16 +88,17 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int m_tiles = (p.m + 255) / 256;
   const int tiles = m_tiles * p.n_tiles;
   const int kn = p.kb_total;
-  const int bufs_used = kn + (p.ext_tiles ? 1 : 0);  // accumulators drained per tile
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&full[s], 1);
       ptx::mbar_init(&empty[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 4; ++b) {
       ptx::mbar_init(&acc_full[b], 1);
-      ptx::mbar_init(&acc_empty[b], 2 * kEpi);
+      ptx::mbar_init(&acc_empty[b], kEpi);
+    }
+    for (int b = 0; b < 2; ++b) {
       ptx::mbar_init(&sc_full[b], 32);
       ptx::mbar_init(&sc_empty[b], kEpi);
     }
@@ -106,6 +120,8 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
 
   // (The loops of the two issuing threads step the stage, its phase and the
   // descriptors with adds only: see f8_gemm.cu.)
+  if (warp < kRoleWarps) {
+  ptx::setmaxnreg_dec<40>();
   if (warp == 0 && ptx::elect_one()) {
     // ------------------------------------------------------ TMA producer
     int it = 0, s = 0;
@@ -168,9 +184,13 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const uint64_t rd0 = ptx::sw128_desc(b_addr, p.ext_mn ? 8192 : 16, 1024);
     const uint64_t bs = p.b_mn ? (4096 >> 4) : (32 >> 4);
     const uint64_t rs = p.ext_mn ? (2048 >> 4) : (32 >> 4);
+    // the second 64 of this CTA's 128 B rows (columns of C): 64 rows of 128 bytes
+    // further where K-major, 64 bytes further in every row where MN-major; the LoRA
+    // operand's 64 columns are a box of their own either way
+    const uint64_t bh = p.b_mn ? (64 >> 4) : (8192 >> 4), rh = 8192 >> 4;
     const uint32_t idesc = p.idesc;
     int s = 0;
-    uint32_t ph = 0, b = 0, bph = 1;
+    uint32_t ph = 0, b = 0, bph = 1;  // b: accumulator 0 or 2 of a block's first half
     uint64_t off = 0;
     bool ok = true;
     auto next = [&]() {
@@ -182,43 +202,58 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       }
     };
     auto next_acc = [&]() {
-      b ^= 1;
+      b ^= 2;
       if (b == 0) bph ^= 1;
     };
     for (int t = pair; t < tiles && ok; t += pairs) {
       for (int i = 0; i < kn; ++i) {
-        ok = ptx::mbar_wait(&acc_empty[b], bph, kTimeoutCycles, abort_flag) &&
-             ptx::mbar_wait(&full[s], ph, kTimeoutCycles, abort_flag);
+        // the operands first: they are there long before the accumulator is free
+        ok = ptx::mbar_wait(&full[s], ph, kTimeoutCycles, abort_flag) &&
+             ptx::mbar_wait(&acc_empty[b], bph, kTimeoutCycles, abort_flag);
         if (!ok) break;
         ptx::tc_fence_after();
-        const uint32_t d = tmem + b * 256;
         const uint64_t ad = ad0 + off, bd = bd0 + off;
+        uint32_t d = tmem + b * 128;
         ptx::umma_f8_pair(d, ad, bd, idesc, 0u);
         ptx::umma_f8_pair(d, ad + 2, bd + bs, idesc, 1u);
         ptx::umma_f8_pair(d, ad + 4, bd + 2 * bs, idesc, 1u);
         ptx::umma_f8_pair(d, ad + 6, bd + 3 * bs, idesc, 1u);
-        ptx::umma_commit_pair(&empty[s]);
         ptx::umma_commit_pair(&acc_full[b]);
+        ok = ptx::mbar_wait(&acc_empty[b + 1], bph, kTimeoutCycles, abort_flag);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        d += 128;
+        ptx::umma_f8_pair(d, ad, bd + bh, idesc, 0u);
+        ptx::umma_f8_pair(d, ad + 2, bd + bh + bs, idesc, 1u);
+        ptx::umma_f8_pair(d, ad + 4, bd + bh + 2 * bs, idesc, 1u);
+        ptx::umma_f8_pair(d, ad + 6, bd + bh + 3 * bs, idesc, 1u);
+        ptx::umma_commit_pair(&acc_full[b + 1]);
+        ptx::umma_commit_pair(&empty[s]);
         next();
         next_acc();
       }
       if (p.ext_tiles && ok) {
-        // every LoRA stage goes into one accumulator
-        ok = ptx::mbar_wait(&acc_empty[b], bph, kTimeoutCycles, abort_flag);
+        // every LoRA stage goes into one pair of accumulators
+        ok = ptx::mbar_wait(&acc_empty[b], bph, kTimeoutCycles, abort_flag) &&
+             ptx::mbar_wait(&acc_empty[b + 1], bph, kTimeoutCycles, abort_flag);
         for (int x = 0, h = 0; x < p.ext_tiles && ok; ++x) {
           ok = ptx::mbar_wait(&full[s], ph, kTimeoutCycles, abort_flag);
           if (!ok) break;
           ptx::tc_fence_after();
           const int steps = ++h == p.ext_half ? p.ext_last_steps : 4;
           if (h == p.ext_half) h = 0;
-          for (int ks = 0; ks < steps; ++ks)
-            ptx::umma_bf16_pair(tmem + b * 256, ad0 + off + 2 * ks, rd0 + off + rs * ks,
-                                p.idesc_ext, (x | ks) != 0 ? 1u : 0u);
+          for (int ks = 0; ks < steps; ++ks) {
+            const uint64_t ad = ad0 + off + 2 * ks, rd = rd0 + off + rs * ks;
+            const uint32_t acc = (x | ks) != 0 ? 1u : 0u;
+            ptx::umma_bf16_pair(tmem + b * 128, ad, rd, p.idesc_ext, acc);
+            ptx::umma_bf16_pair(tmem + b * 128 + 128, ad, rd + rh, p.idesc_ext, acc);
+          }
           ptx::umma_commit_pair(&empty[s]);
           next();
         }
         if (!ok) break;
         ptx::umma_commit_pair(&acc_full[b]);
+        ptx::umma_commit_pair(&acc_full[b + 1]);
         next_acc();
       }
     }
@@ -242,63 +277,80 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       }
     }
     f8::cp_async_wait_all();
-  } else if (warp >= kRoleWarps) {
+  }
+  } else {
     // ------------------------------------------------------ sums
-    const int quarter = warp & 3, half = (warp - kRoleWarps) >> 2;
-    const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
-    const uint32_t leader_empty = ptx::cluster_addr(&acc_empty[0], 0);
+    ptx::setmaxnreg_inc<232>();
+    // warps 4-7 add the accumulators of the first half of each block, warps 8-11
+    // those of the second: columns [64 h, 64 h + 64) and [128 + 64 h, ...) of the tile
+    const int quarter = warp & 3, h = (warp - kRoleWarps) >> 2;
     const int lrow = 32 * quarter + lane;
-    int use = 0, chunk = 0;
-    bool ok = true;
+    const uint32_t tmem_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + h * 128;
+    const uint32_t full_base = ptx::smem_u32(&acc_full[h]);
+    const uint32_t free_base = ptx::cluster_addr(&acc_empty[h], 0);
+    const uint32_t sa_base = ptx::smem_u32(&ring->a[0][0][lrow]);
+    const uint32_t sb_base = ptx::smem_u32(&ring->b[0][0][0]);
+    // two sums a register pair: one instruction multiplies and adds both
+    uint64_t acc[64];
+    uint32_t use = 0, chunk = 0;
+    bool ok = true, ready = false;
+    // Adds one finished accumulator, its first 64 columns times s0, the others times s1.
+    auto add_block = [&](float s0, float s1) {
+      if (!ready) {
+        ok = ptx::mbar_wait(&acc_full[2 * (use & 1) + h], (use >> 1) & 1, kTimeoutCycles,
+                            abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+      }
+      ptx::tc_fence_after();
+      const uint32_t at = tmem_base + (use & 1) * 256, release = free_base + (use & 1) * 16;
+      ++use;
+      uint32_t r[64];
+      ptx::tmem_ld_x64(at, r);
+      ptx::tmem_ld_wait(r);
+      add64(acc, 0, r, s0);
+      ptx::tmem_ld_x64(at + 64, r);
+      ptx::tmem_ld_wait(r);
+      // everything is in registers: the accumulator may be overwritten
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(release);
+      // the test of the next one takes its time while these are added
+      const bool next = ptx::mbar_test_wait_at(full_base + (use & 1) * 16, (use >> 1) & 1);
+      add64(acc, 32, r, s1);
+      ready = __all_sync(0xffffffffu, next);
+    };
     for (int t = pair; t < tiles; t += pairs) {
       int mt, nt;
       tile_at(p, m_tiles, t, &mt, &nt);
-      // two sums a register pair: one instruction multiplies and adds both
-      uint64_t acc[64];
 #pragma unroll
       for (int j = 0; j < 64; ++j) acc[j] = 0ull;
-      for (int i = 0; i < bufs_used && ok; ++i, ++use) {
-        const int b = use & 1, in = i % f8::kChunk;
-        float s = 1.0f;  // the LoRA term
-        if (i < kn) {
-          if (in == 0)
-            ok = ptx::mbar_wait(&sc_full[chunk & 1], (chunk >> 1) & 1, kTimeoutCycles, abort_flag);
-          s = ring->a[chunk & 1][in][lrow] * ring->b[chunk & 1][in][half];
-        }
-        ok = ok && ptx::mbar_wait(&acc_full[b], (use >> 1) & 1, kTimeoutCycles, abort_flag);
+      for (int k0 = 0; k0 < kn && ok; k0 += f8::kChunk, ++chunk) {
+        ok = ptx::mbar_wait(&sc_full[chunk & 1], (chunk >> 1) & 1, kTimeoutCycles, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        ptx::tc_fence_after();
-        const uint32_t at = tmem + lane_base + b * 256 + half * 128;
-        uint64_t ss;
-        asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
-        uint32_t r[2][16];
-        ptx::tmem_ld_x16(at, r[0]);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          ptx::tmem_ld_wait(r[c & 1]);
-          if (c < 7) ptx::tmem_ld_x16(at + 16 * (c + 1), r[(c + 1) & 1]);
-          if (c == 7) {
-            // everything is in registers: the accumulator may be overwritten
-            ptx::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive_cluster(leader_empty + 8u * b);
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint64_t x;
-            asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(r[c & 1][2 * j]), "r"(r[c & 1][2 * j + 1]));
-            asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[8 * c + j]) : "l"(x), "l"(ss));
-          }
+        uint32_t pa = sa_base + (chunk & 1) * (f8::kChunk * 512);
+        uint32_t pb = sb_base + (chunk & 1) * (f8::kChunk * 8);
+        float sa = ptx::lds_f32(pa);
+        float2 sb = ptx::lds_f32x2(pb);
+        const int n = min(f8::kChunk, kn - k0);
+        for (int i = 0; i < n && ok; ++i) {
+          const float s0 = sa * sb.x, s1 = sa * sb.y;
+          // the next block's scales, on their way while this one is added (the
+          // last read of a chunk runs past it, inside the ring, and is not used)
+          pa += 512;
+          pb += 8;
+          sa = ptx::lds_f32(pa);
+          sb = ptx::lds_f32x2(pb);
+          add_block(s0, s1);
         }
-        if (i < kn && (in == f8::kChunk - 1 || i == kn - 1)) {
-          if (lane == 0) ptx::mbar_arrive(&sc_empty[chunk & 1]);
-          ++chunk;
-        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sc_empty[chunk & 1]);
       }
+      if (p.ext_tiles && ok) add_block(1.0f, 1.0f);  // the LoRA term
       ok = __all_sync(0xffffffffu, ok && !*abort_flag);
       const int row = mt * 256 + static_cast<int>(rank) * 128 + lrow;
-      const int col = nt * 256 + 128 * half;
+      const int col = nt * 256 + 64 * h;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         float v[16];
@@ -307,7 +359,7 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * j]), "=f"(v[2 * j + 1]) : "l"(acc[8 * c + j]));
           if (!ok) v[2 * j] = v[2 * j + 1] = __int_as_float(0x7fffffff);
         }
-        store_run<16>(p, row, col + 16 * c, v);
+        store_run<16>(p, row, col + 128 * (c >> 2) + 16 * (c & 3), v);
       }
     }
   }
@@ -342,8 +394,8 @@ qlora_status f8_gemm_pairs(const qlora_f8& a, const qlora_f8& b, bool trans_b, v
   }
   if (!ok) return QLORA_ERR_CUDA;
   const int fa = a.format == QLORA_E5M2 ? 1 : 0, fb = b.format == QLORA_E5M2 ? 1 : 0;
-  p.idesc = ptx::idesc_f8(fa, fb, 256, 256, 0, p.b_mn);
-  p.idesc_ext = ptx::idesc_bf16(256, 256, 0, p.ext_mn);
+  p.idesc = ptx::idesc_f8(fa, fb, 256, 128, 0, p.b_mn);
+  p.idesc_ext = ptx::idesc_bf16(256, 128, 0, p.ext_mn);
   p.n_tiles = static_cast<int32_t>(ceil_div(n, 256));
   const int64_t tiles = ceil_div(m, 256) * p.n_tiles;
   if (tiles > 0x3fffffff) return QLORA_ERR_SHAPE;

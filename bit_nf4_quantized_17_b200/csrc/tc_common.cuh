@@ -11,7 +11,7 @@ namespace qlora {
 
 // 2-D tensor map over a row-major matrix of `outer` rows x `inner` elements
 // (bf16 or bytes), row stride `ld` elements, box box_inner x box_outer,
-// optionally 128-byte swizzled.
+// optionally swizzled: by 128 bytes, or by 64 where the box is 64 bytes wide.
 bool make_map(CUtensorMap* map, const void* base, bool bf16, uint64_t inner, uint64_t outer,
               uint64_t ld, uint32_t box_inner, uint32_t box_outer, bool swizzle);
 
