@@ -295,7 +295,7 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     uint32_t use = 0, chunk = 0;
     bool ok = true, ready = false;
     // Adds one finished accumulator, its first 64 columns times s0, the others times s1.
-    auto add_block = [&](float s0, float s1) {
+    auto add_block = [&](float s0, float s1, auto&& prefetch) {
       if (!ready) {
         ok = ptx::mbar_wait(&acc_full[2 * (use & 1) + h], (use >> 1) & 1, kTimeoutCycles,
                             abort_flag);
@@ -315,8 +315,11 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster(release);
-      // the test of the next one takes its time while these are added
+      // the test of the next one, and its scales, take their time while these are
+      // added: next to the MMAs' operand reads an access to shared memory takes
+      // 100 to 250 cycles
       const bool next = ptx::mbar_test_wait_at(full_base + (use & 1) * 16, (use >> 1) & 1);
+      prefetch();
       add64(acc, 32, r, s1);
       ready = __all_sync(0xffffffffu, next);
     };
@@ -340,14 +343,15 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           // last read of a chunk runs past it, inside the ring, and is not used)
           pa += 512;
           pb += 8;
-          sa = ptx::lds_f32(pa);
-          sb = ptx::lds_f32x2(pb);
-          add_block(s0, s1);
+          add_block(s0, s1, [&]() {
+            sa = ptx::lds_f32(pa);
+            sb = ptx::lds_f32x2(pb);
+          });
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sc_empty[chunk & 1]);
       }
-      if (p.ext_tiles && ok) add_block(1.0f, 1.0f);  // the LoRA term
+      if (p.ext_tiles && ok) add_block(1.0f, 1.0f, []() {});  // the LoRA term
       ok = __all_sync(0xffffffffu, ok && !*abort_flag);
       const int row = mt * 256 + static_cast<int>(rank) * 128 + lrow;
       const int col = nt * 256 + 64 * h;
