@@ -12,7 +12,7 @@
 // One CTA computes a 128 x BN tile from a 128-row operand P and a BN-row
 // operand Q; both roles can be played by A and B:
 //   * P = A, Q = B (BN = 128): thread = output row, one scale per thread and block;
-//   * SWAP, for few tokens: P = B, Q = A (BN = 16, 32, 64): the 128 rows of the
+//   * SWAP, for few tokens: P = B, Q = A (BN = 16, 32): the 128 rows of the
 //     MMA are output columns, no MMA row is wasted on tokens that do not exist,
 //     and B, whose bytes bound the product, is read once.  A thread holds one
 //     output column and all BN tokens.
@@ -51,7 +51,9 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
 
 template <int BN, bool SWAP>
 struct Cfg {
+  static_assert(SWAP ? BN <= 32 : BN == 128, "the column split of the epilogue");
   static constexpr int kEpi = BN >= 128 ? 8 : 4;  // epilogue warps
+  static constexpr int kPerSm = SWAP ? 2 : 1;
   static constexpr int kThreads = 128 + 32 * kEpi;  // TMA, MMA, scales, one idle; the sums
   static constexpr int kCols = BN / (kEpi / 4);   // accumulator columns per thread
   static constexpr int kBufs = BN >= 128 ? 2 : 4; // TMEM accumulators in flight
@@ -65,7 +67,7 @@ struct Cfg {
 };
 
 template <int BN, bool SWAP>
-__global__ void __launch_bounds__(Cfg<BN, SWAP>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<BN, SWAP>::kThreads, Cfg<BN, SWAP>::kPerSm)
 f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ CUtensorMap tmQ,
                const __grid_constant__ CUtensorMap tmP2, const __grid_constant__ CUtensorMap tmQ2,
                const GemmArgs p) {
@@ -90,14 +92,12 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t S = gridDim.z, z = blockIdx.z;  // the cluster spans z
   // tile of P (128 rows) and of Q (BN rows)
-  const int qt = SWAP ? blockIdx.x / p.n_tiles : blockIdx.x % p.n_tiles;
-  const int pt = SWAP ? blockIdx.x % p.n_tiles : blockIdx.x / p.n_tiles;
+  const int qt = blockIdx.x % p.n_tiles, pt = blockIdx.x / p.n_tiles;
   const int p0 = pt * 128, q0 = qt * BN;
   const int kb0 = static_cast<int>(z) * p.kb_per;
   const int kn = max(0, min(p.kb_per, p.kb_total - kb0));
   // the LoRA stages belong to the last split
   const int ext = (z == S - 1) ? p.ext_tiles : 0;
-  const int bufs_used = kn + (ext ? 1 : 0);  // accumulators drained, in order
   const bool p_mn = SWAP && p.b_mn, q_mn = !SWAP && p.b_mn;
   const bool p2_mn = SWAP && p.ext_mn, q2_mn = !SWAP && p.ext_mn;
 
@@ -277,51 +277,78 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
     f8::cp_async_wait_all();
   } else if (warp >= 4) {
     // ------------------------------------------------------ epilogue warps
-    const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
     const int row = 32 * quarter + lane;  // row of the P tile
-    int chunk = 0;
-    for (int i = 0; i < bufs_used; ++i) {
-      const int b = i % C::kBufs, in = i % f8::kChunk;  // (both powers of two)
-      const bool lora = i == kn;
-      if (!lora && in == 0)
-        ok = ptx::mbar_wait(&sc_full[chunk & 1], (chunk >> 1) & 1, kTimeoutCycles, abort_flag);
-      ok = ok && ptx::mbar_wait(&acc_full[b], (i / C::kBufs) & 1, kTimeoutCycles, abort_flag);
+    const uint32_t tmem_base = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + half * C::kCols;
+    int use = 0;
+    auto wait_acc = [&]() {
+      ok = ptx::mbar_wait(&acc_full[use % C::kBufs], (use / C::kBufs) & 1, kTimeoutCycles,
+                          abort_flag);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      ptx::tc_fence_after();
-      const float* sa = ring->a[chunk & 1][in];
-      const float sb = lora ? 1.0f : ring->b[chunk & 1][in][0];
-      const float s_row = (SWAP || lora) ? 1.0f : sa[row] * sb;
-      const uint32_t at = tmem + lane_base + b * BN + half * C::kCols;
-      uint32_t r[2][16];
-      ptx::tmem_ld_x16(at, r[0]);
-#pragma unroll
-      for (int c = 0; c < C::kCols / 16; ++c) {
-        ptx::tmem_ld_wait(r[c & 1]);
-        if (c + 1 < C::kCols / 16) ptx::tmem_ld_x16(at + 16 * (c + 1), r[(c + 1) & 1]);
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          float4 s = make_float4(s_row, s_row, s_row, s_row);
-          if (SWAP && !lora) {
-            s = *reinterpret_cast<const float4*>(sa + 16 * c + j);  // one address for all lanes
-            s.x *= sb;
-            s.y *= sb;
-            s.z *= sb;
-            s.w *= sb;
-          }
-          acc[16 * c + j] = fmaf(__uint_as_float(r[c & 1][j]), s.x, acc[16 * c + j]);
-          acc[16 * c + j + 1] = fmaf(__uint_as_float(r[c & 1][j + 1]), s.y, acc[16 * c + j + 1]);
-          acc[16 * c + j + 2] = fmaf(__uint_as_float(r[c & 1][j + 2]), s.z, acc[16 * c + j + 2]);
-          acc[16 * c + j + 3] = fmaf(__uint_as_float(r[c & 1][j + 3]), s.w, acc[16 * c + j + 3]);
-        }
-      }
+      if (ok) ptx::tc_fence_after();
+    };
+    auto release_acc = [&]() {
       ptx::tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        ptx::mbar_arrive(&acc_empty[b]);
-        if (!lora && (in == f8::kChunk - 1 || i == kn - 1)) ptx::mbar_arrive(&sc_empty[chunk & 1]);
+      if (lane == 0) ptx::mbar_arrive(&acc_empty[use % C::kBufs]);
+      ++use;
+    };
+    // Adds one finished accumulator: each column (SWAP: token) j times s[j] sb with
+    // the tokens' scales s in shared memory, or the thread's row times sb.
+    uint64_t pairs[SWAP ? 1 : 32];
+#pragma unroll
+    for (int j = 0; j < (SWAP ? 1 : 32); ++j) pairs[j] = 0ull;
+    auto add_block = [&](const float* s, float sb) {
+      wait_acc();
+      if (!ok) return;
+      const uint32_t at = tmem_base + (use % C::kBufs) * BN;
+      if (!SWAP) {
+        uint32_t r[64];
+        ptx::tmem_ld_x64(at, r);
+        ptx::tmem_ld_wait(r);
+        release_acc();
+        f8::add64(pairs, 0, r, sb);
+      } else {
+        uint32_t r[C::kCols / 16][16];
+#pragma unroll
+        for (int c = 0; c < C::kCols / 16; ++c) ptx::tmem_ld_x16(at + 16 * c, r[c]);
+#pragma unroll
+        for (int c = 0; c < C::kCols / 16; ++c) ptx::tmem_ld_wait(r[c]);
+        release_acc();
+#pragma unroll
+        for (int j = 0; j < C::kCols; j += 4) {
+          float4 f = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+          if (s) f = *reinterpret_cast<const float4*>(s + j);  // one address for all lanes
+          acc[j] = fmaf(__uint_as_float(r[j / 16][j % 16]), f.x * sb, acc[j]);
+          acc[j + 1] = fmaf(__uint_as_float(r[j / 16][j % 16 + 1]), f.y * sb, acc[j + 1]);
+          acc[j + 2] = fmaf(__uint_as_float(r[j / 16][j % 16 + 2]), f.z * sb, acc[j + 2]);
+          acc[j + 3] = fmaf(__uint_as_float(r[j / 16][j % 16 + 3]), f.w * sb, acc[j + 3]);
+        }
       }
-      if (in == f8::kChunk - 1) ++chunk;
+    };
+    for (int k0 = 0, chunk = 0; k0 < kn && ok; k0 += f8::kChunk, ++chunk) {
+      const int slot = chunk & 1;
+      ok = ptx::mbar_wait(&sc_full[slot], (chunk >> 1) & 1, kTimeoutCycles, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      const int n = min(f8::kChunk, kn - k0);
+      float sa = SWAP ? 1.0f : ring->a[slot][0][row], sb = ring->b[slot][0][0];
+      for (int i = 0; i < n && ok; ++i) {
+        const float s = sa * sb;
+        // the next block's scales (the last read of a chunk is not used)
+        const int ni = min(i + 1, f8::kChunk - 1);
+        if (!SWAP) sa = ring->a[slot][ni][row];
+        sb = ring->b[slot][ni][0];
+        add_block(ring->a[slot][i], s);
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sc_empty[slot]);
+    }
+    if (ext && ok) add_block(nullptr, 1.0f);  // the LoRA term
+    if (!SWAP) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        asm("mov.b64 {%0, %1}, %2;"
+            : "=f"(acc[(2 * j) % C::kCols]), "=f"(acc[(2 * j + 1) % C::kCols])
+            : "l"(pairs[SWAP ? 0 : j]));
     }
     ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     if (!ok) {
@@ -402,9 +429,18 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
   }
 }
 
+// Contraction splits for `tiles` output tiles on `slots` CTAs: as many as run at
+// once (a cluster holds at most 8), at least 4 blocks each.  (More splits than fit at
+// once never pay: clusters wait for whole groups of free SMs.  64 x 11008 x 4096, 86
+// tiles on 148 SMs: 14 us unsplit, 40 us in 5 splits.)
+int split_count(int64_t tiles, int64_t kb, int64_t slots) {
+  const int64_t s = std::min<int64_t>({8, slots / tiles, kb / 4});
+  return static_cast<int>(std::max<int64_t>(1, s));
+}
+
 template <int BN, bool SWAP>
 qlora_status launch(const qlora_f8& a, const qlora_f8& b, bool trans_b, GemmArgs p,
-                    const F8Lora& l, int splits, cudaStream_t s) {
+                    const F8Lora& l, cudaStream_t s) {
   using C = Cfg<BN, SWAP>;
   const int64_t m = p.m, n = p.n;
   CUtensorMap ma, mb, ml, mr;
@@ -427,14 +463,17 @@ qlora_status launch(const qlora_f8& a, const qlora_f8& b, bool trans_b, GemmArgs
                  : ptx::idesc_f8(fa, fb, 128, BN, 0, p.b_mn);
   p.idesc_ext = SWAP ? ptx::idesc_bf16(128, BN, p.ext_mn, 0)
                      : ptx::idesc_bf16(128, BN, 0, p.ext_mn);
-  p.kb_per = static_cast<int32_t>(ceil_div(p.kb_total, splits));
-  // the stages that fit; no more than a split has blocks
-  const int64_t want = p.kb_per + p.ext_tiles;
-  p.stages = static_cast<int32_t>(
-      std::min<int64_t>({kMaxStages, want, (200 * 1024) / C::kStage}));
   const int64_t p_tiles = ceil_div(SWAP ? n : m, 128), q_tiles = ceil_div(SWAP ? m : n, BN);
-  p.n_tiles = static_cast<int32_t>(SWAP ? p_tiles : q_tiles);
+  p.n_tiles = static_cast<int32_t>(q_tiles);
   if (p_tiles * q_tiles > 0x7fffffff) return QLORA_ERR_SHAPE;
+  const int sms = f8::sm_count();
+  const int splits = split_count(p_tiles * q_tiles, p.kb_total, C::kPerSm * sms);
+  p.kb_per = static_cast<int32_t>(ceil_div(p.kb_total, splits));
+  // the stages that fit beside as many CTAs as an SM gets; no more than a split has blocks
+  const int64_t want = p.kb_per + p.ext_tiles;
+  const bool two = C::kPerSm == 2 && p_tiles * q_tiles * splits > sms;
+  p.stages = static_cast<int32_t>(
+      std::min<int64_t>({kMaxStages, want, ((two ? 100 : 200) * 1024) / C::kStage}));
   const void* fn = reinterpret_cast<const void*>(f8_gemm_kernel<BN, SWAP>);
   const qlora_status cs = ensure_smem(fn, 220 * 1024);
   if (cs != QLORA_OK) return cs;
@@ -459,16 +498,6 @@ qlora_status launch(const qlora_f8& a, const qlora_f8& b, bool trans_b, GemmArgs
     return QLORA_ERR_CUDA;
   }
   return after_launch("f8_gemm", s);
-}
-
-// Contraction splits for `tiles` output tiles: as many CTAs as there are SMs,
-// a cluster of at most 8, at least 4 blocks each.
-int split_count(int64_t tiles, int64_t kb) {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    (void)cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t s = std::min<int64_t>({8, sms / tiles, kb / 4});
-  return static_cast<int>(std::max<int64_t>(1, s));
 }
 
 }  // namespace
@@ -501,15 +530,24 @@ qlora_status f8_gemm(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c
                      const F8Lora& l, cudaStream_t s) {
   const GemmArgs p = f8::gemm_args(a, b, trans_b, c, c_f32, l);
   const int64_t m = p.m, n = p.n;
-  if (m <= 64) {
-    const int splits = split_count(ceil_div(n, 128), p.kb_total);
-    if (m <= 16) return launch<16, true>(a, b, trans_b, p, l, splits, s);
-    if (m <= 32) return launch<32, true>(a, b, trans_b, p, l, splits, s);
-    return launch<64, true>(a, b, trans_b, p, l, splits, s);
-  }
+  if (m <= 16) return launch<16, true>(a, b, trans_b, p, l, s);
+  if (m <= 32) return launch<32, true>(a, b, trans_b, p, l, s);
+  // single CTAs or pairs, whichever ends sooner: a pair's 256 x 256 block takes 1.5
+  // times a CTA's 128 x 128 block (0.47 against 0.32 us).  At k = 4096: 384 x 11008
+  // in 28 us on CTAs, 42 us on pairs; 4096 x 4096 in 112 and 76 us.
+  const int sms = f8::sm_count();
   const int64_t tiles = ceil_div(n, 128) * ceil_div(m, 128);
-  if (tiles > 148) return f8_gemm_pairs(a, b, trans_b, c, c_f32, l, s);
-  return launch<128, false>(a, b, trans_b, p, l, split_count(tiles, p.kb_total), s);
+  const int64_t one = ceil_div(tiles, sms);
+  const int64_t two = ceil_div(ceil_div(n, 256) * ceil_div(m, 256), sms / 2);
+  if (tiles > sms && 2 * one > 3 * two) return f8_gemm_pairs(a, b, trans_b, c, c_f32, l, s);
+  return launch<128, false>(a, b, trans_b, p, l, s);
+}
+
+int f8::sm_count() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    (void)cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
 }
 
 }  // namespace qlora

@@ -77,6 +77,20 @@ static __device__ __forceinline__ void fill_scales(const GemmArgs& p, ScaleRing<
   cp_async_arrive(full);
 }
 
+// acc[at ..] += s r, two sums in a register pair and instruction.
+template <int N>
+static __device__ __forceinline__ void add64(uint64_t (&acc)[N], int at, const uint32_t (&r)[64],
+                                             float s) {
+  uint64_t ss;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    uint64_t x;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(r[2 * j]), "r"(r[2 * j + 1]));
+    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[at + j]) : "l"(x), "l"(ss));
+  }
+}
+
 // N consecutive columns of a row of C from column c0 (N = 4 or 16)
 template <int N>
 static __device__ __forceinline__ void store_run(const GemmArgs& p, int64_t row, int64_t c0,
@@ -115,6 +129,9 @@ static __device__ __forceinline__ void store_run(const GemmArgs& p, int64_t row,
     }
   }
 }
+
+// SMs of the current device.
+int sm_count();
 
 // The fields of the arguments that do not depend on the kernel.
 GemmArgs gemm_args(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,

@@ -31,6 +31,7 @@ namespace {
 
 using f8::GemmArgs;
 using f8::kTimeoutCycles;
+using f8::add64;
 using f8::store_run;
 
 constexpr int kEpi = 8;
@@ -49,19 +50,6 @@ __device__ __forceinline__ void tile_at(const GemmArgs& p, int m_tiles, int t, i
   const int rows = min(kGroup, m_tiles - g * kGroup);
   *nt = in / rows;
   *mt = g * kGroup + in - *nt * rows;
-}
-
-// acc[at ..] += s r, two sums an instruction.
-__device__ __forceinline__ void add64(uint64_t (&acc)[64], int at, const uint32_t (&r)[64],
-                                      float s) {
-  uint64_t ss;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "f"(s));
-#pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    uint64_t x;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(r[2 * j]), "r"(r[2 * j + 1]));
-    asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc[at + j]) : "l"(x), "l"(ss));
-  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)

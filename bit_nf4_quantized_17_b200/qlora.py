@@ -7,7 +7,6 @@ in the library's CUDA kernels.  A missing library raises immediately: there
 is no other implementation to fall back to.
 """
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -521,6 +520,8 @@ class F8Matrix:
     """Caller-owned device arrays of a matrix held in 8 bits (see qlora_f8): codes (uint8,
     rows x ld) and scales (fp32: blocks x rows, or row blocks x column blocks for tiles)."""
 
+    __slots__ = ("rows", "cols", "layout", "format", "pow2", "codes", "scales", "struct")
+
     def __init__(self, rows, cols, layout, format, pow2, codes, scales):
         if layout not in (QLORA_F8_ROWS, QLORA_F8_TILES) or format not in _F8_DTYPE:
             raise ValueError(f"layout {layout}, format {format}: expected QLORA_F8_ROWS or "
@@ -536,20 +537,27 @@ class F8Matrix:
             raise ValueError(f"scales: expected a contiguous fp32 tensor of shape {shape} beside "
                              f"the codes, got {scales.dtype} {tuple(scales.shape)} on "
                              f"{scales.device}")
+        self._set(rows, cols, layout, format, pow2, codes, scales, codes.shape[1])
+
+    def _set(self, rows, cols, layout, format, pow2, codes, scales, ld):
         self.rows, self.cols, self.layout, self.format = rows, cols, layout, format
         self.pow2, self.codes, self.scales = bool(pow2), codes, scales
-        self.struct = qlora_f8(rows, cols, codes.shape[1], layout, format, int(self.pow2), 0,
-                               codes.data_ptr(), scales.data_ptr())
+        self.struct = qlora_f8(rows, cols, ld, layout, format, self.pow2, 0, codes.data_ptr(),
+                               scales.data_ptr())
 
     @classmethod
     def empty(cls, rows, cols, layout=QLORA_F8_ROWS, format=QLORA_E4M3, pow2=False,
               device="cuda"):
-        if rows < 0 or cols < 1:
-            raise ValueError(f"a matrix of {rows} x {cols}")
-        return cls(rows, cols, layout, format, pow2,
-                   torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.uint8, device=device),
-                   torch.empty(_f8_scales_shape(rows, cols, layout), dtype=torch.float32,
-                               device=device))
+        if (rows < 0 or cols < 1 or layout not in (QLORA_F8_ROWS, QLORA_F8_TILES)
+                or format not in _F8_DTYPE):
+            raise ValueError(f"a matrix of {rows} x {cols}, layout {layout}, format {format}")
+        m = cls.__new__(cls)
+        ld = (cols + 15) // 16 * 16
+        m._set(rows, cols, layout, format, pow2,
+               torch.empty((rows, ld), dtype=torch.uint8, device=device),
+               torch.empty(_f8_scales_shape(rows, cols, layout), dtype=torch.float32,
+                           device=device), ld)
+        return m
 
     @property
     def values(self):
@@ -562,17 +570,33 @@ class F8Matrix:
         return self.codes.numel() + 4 * self.scales.numel()
 
 
-def _on_current_device(*tensors):
-    """The library launches on the current device: refuse tensors that live elsewhere."""
+def _device_stream(stream, *tensors):
+    """The raw stream to launch on.  The library launches on the current device: tensors that
+    live elsewhere are refused."""
     dev = torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.device.index != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the current device is cuda:{dev}")
+    return stream.cuda_stream
 
 
-def _in_stream(stream):
-    """Allocate for work on `stream`: memory taken here is reused in that stream's order."""
-    return torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+def _empty_in(stream, shape, dtype, device):
+    """A tensor for work on `stream`: its memory is reused in that stream's order."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _workspace_in(stream, nbytes, device):
+    if stream is None:
+        return _workspace(nbytes, device)
+    with torch.cuda.stream(stream):
+        return _workspace(nbytes, device)
 
 
 def qlora_f8_quantize(X, layout=QLORA_F8_ROWS, format=QLORA_E4M3, pow2=False, out=None,
@@ -584,12 +608,15 @@ def qlora_f8_quantize(X, layout=QLORA_F8_ROWS, format=QLORA_E4M3, pow2=False, ou
                          f"{tuple(X.shape)} on {X.device}")
     rows, cols = X.shape
     if out is None:
-        with _in_stream(stream):
+        if stream is None:
             out = F8Matrix.empty(rows, cols, layout, format, pow2, X.device)
+        else:
+            with torch.cuda.stream(stream):
+                out = F8Matrix.empty(rows, cols, layout, format, pow2, X.device)
     elif (out.rows, out.cols) != (rows, cols):
         raise ValueError(f"out holds a {out.rows} x {out.cols} matrix, X is {rows} x {cols}")
-    _on_current_device(X, out.codes)
-    _ok(lib().qlora_f8_quantize(X.data_ptr(), _DTYPE[X.dtype], out.struct, _stream(stream)),
+    s = _device_stream(stream, X, out.codes)
+    _ok(lib().qlora_f8_quantize(X.data_ptr(), _DTYPE[X.dtype], out.struct, s),
         "qlora_f8_quantize")
     return out
 
@@ -598,8 +625,7 @@ def _f8_out(out, shape, dtype, device, stream, name):
     if out is None:
         if dtype not in _DTYPE:
             raise ValueError(f"{name}: fp32 or bf16, not {dtype}")
-        with _in_stream(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
+        return _empty_in(stream, shape, dtype, device)
     if (tuple(out.shape) != shape or out.dtype not in _DTYPE or not out.is_contiguous()
             or out.device != device):
         raise ValueError(f"{name}: expected a contiguous fp32 or bf16 tensor of shape {shape} on "
@@ -610,8 +636,8 @@ def _f8_out(out, shape, dtype, device, stream, name):
 def qlora_f8_dequantize(q, dtype=torch.bfloat16, out=None, stream=None):
     """The values of an F8Matrix, code times scale, as a bf16 or fp32 tensor."""
     out = _f8_out(out, (q.rows, q.cols), dtype, q.codes.device, stream, "out")
-    _on_current_device(q.codes)
-    _ok(lib().qlora_f8_dequantize(q.struct, out.data_ptr(), _DTYPE[out.dtype], _stream(stream)),
+    s = _device_stream(stream, q.codes)
+    _ok(lib().qlora_f8_dequantize(q.struct, out.data_ptr(), _DTYPE[out.dtype], s),
         "qlora_f8_dequantize")
     return out
 
@@ -623,9 +649,9 @@ def qlora_f8_matmul(a, b, trans_b=True, dtype=torch.bfloat16, out=None, stream=N
         raise ValueError(f"a is {a.rows} x {a.cols}, b is {b.rows} x {b.cols} "
                          f"({'transposed' if trans_b else 'not transposed'})")
     out = _f8_out(out, (a.rows, n), dtype, a.codes.device, stream, "out")
-    _on_current_device(a.codes, b.codes)
+    s = _device_stream(stream, a.codes, b.codes)
     _ok(lib().qlora_f8_matmul(a.struct, b.struct, 1 if trans_b else 0, out.data_ptr(),
-                              _DTYPE[out.dtype], _stream(stream)), "qlora_f8_matmul")
+                              _DTYPE[out.dtype], s), "qlora_f8_matmul")
     return out
 
 
@@ -637,13 +663,12 @@ def qlora_linear_bwd_f8_workspace(M, N, K, r):
 
 
 def _grads(M, N, K, r, device, want_dx, dX, dA, dB, stream):
-    with _in_stream(stream):
-        if want_dx and dX is None:
-            dX = torch.empty((M, K), dtype=torch.bfloat16, device=device)
-        if dA is None:
-            dA = torch.empty((r, K), dtype=torch.float32, device=device)
-        if dB is None:
-            dB = torch.empty((N, r), dtype=torch.float32, device=device)
+    if want_dx and dX is None:
+        dX = _empty_in(stream, (M, K), torch.bfloat16, device)
+    if dA is None:
+        dA = _empty_in(stream, (r, K), torch.float32, device)
+    if dB is None:
+        dB = _empty_in(stream, (N, r), torch.float32, device)
     return (dX if want_dx else None), dA, dB
 
 
@@ -662,14 +687,15 @@ def qlora_linear_bwd_f8(q, A, B, r, alpha, X8, U, dY, adapter=None, p=0.0, keep_
     o = _opts(r, A, adapter, p, keep_mask, None)
     _check_linear(q, M, rt, A=A, B=B, U=U, dY=dY, dX=dX, dA=dA, dB=dB, adapter=adapter,
                   keep_mask=keep_mask)
-    _on_current_device(q.codes, X8.codes, A, B, U, dY, dX, dA, dB, adapter, keep_mask, workspace)
+    s = _device_stream(stream, q.codes, X8.codes, A, B, U, dY, dX, dA, dB, adapter, keep_mask,
+                       workspace)
     if workspace is None:
-        with _in_stream(stream):
-            workspace = _workspace(qlora_linear_bwd_f8_workspace(M, q.rows, q.cols, rt), dev)
+        workspace = _workspace_in(stream, qlora_linear_bwd_f8_workspace(M, q.rows, q.cols, rt),
+                                  dev)
     _ok(lib().qlora_linear_bwd_f8(q.struct, _ptr(A), _ptr(B), r, float(alpha), o, X8.struct,
                                   _ptr(U), _ptr(dY), _ptr(dX), _ptr(dA), _ptr(dB),
-                                  1 if accumulate else 0, _ptr(workspace), workspace.numel(),
-                                  _stream(stream)), "qlora_linear_bwd_f8")
+                                  1 if accumulate else 0, _ptr(workspace), workspace.numel(), s),
+        "qlora_linear_bwd_f8")
     if check:
         qlora_check(workspace, stream)
     return dX, dA, dB
@@ -698,16 +724,15 @@ def qlora_f8_linear_fwd(W, A, B, alpha, X, X8, Y=None, U_save=None, workspace=No
     M, r = X8.rows, A.shape[0]
     _check_f8_base(W, X8)
     if Y is None:
-        with _in_stream(stream):
-            Y = torch.empty((M, W.rows), dtype=torch.bfloat16, device=X.device)
+        Y = _empty_in(stream, (M, W.rows), torch.bfloat16, X.device)
     _check_linear(W, M, r, A=A, B=B, X=X, Y=Y, U=U_save)
-    _on_current_device(W.codes, A, B, X, X8.codes, Y, U_save, workspace)
+    s = _device_stream(stream, W.codes, A, B, X, X8.codes, Y, U_save, workspace)
     if workspace is None:
-        with _in_stream(stream):
-            workspace = _workspace(qlora_f8_linear_workspace(M, W.rows, W.cols, r)[0], X.device)
+        workspace = _workspace_in(stream, qlora_f8_linear_workspace(M, W.rows, W.cols, r)[0],
+                                  X.device)
     _ok(lib().qlora_f8_linear_fwd(W.struct, _ptr(A), _ptr(B), r, float(alpha), _ptr(X), X8.struct,
-                                  _ptr(Y), _ptr(U_save), _ptr(workspace), workspace.numel(),
-                                  _stream(stream)), "qlora_f8_linear_fwd")
+                                  _ptr(Y), _ptr(U_save), _ptr(workspace), workspace.numel(), s),
+        "qlora_f8_linear_fwd")
     if check:
         qlora_check(workspace, stream)
     return Y
@@ -724,14 +749,13 @@ def qlora_f8_linear_bwd(W, A, B, alpha, X8, U, dY, grad_format=QLORA_E5M2, dX=No
         raise ValueError("U: the forward's X A^T is needed, X is not kept")
     dX, dA, dB = _grads(M, W.rows, W.cols, r, dev, want_dx, dX, dA, dB, stream)
     _check_linear(W, M, r, A=A, B=B, U=U, dY=dY, dX=dX, dA=dA, dB=dB)
-    _on_current_device(W.codes, X8.codes, A, B, U, dY, dX, dA, dB, workspace)
+    s = _device_stream(stream, W.codes, X8.codes, A, B, U, dY, dX, dA, dB, workspace)
     if workspace is None:
-        with _in_stream(stream):
-            workspace = _workspace(qlora_f8_linear_workspace(M, W.rows, W.cols, r)[1], dev)
+        workspace = _workspace_in(stream, qlora_f8_linear_workspace(M, W.rows, W.cols, r)[1], dev)
     _ok(lib().qlora_f8_linear_bwd(W.struct, _ptr(A), _ptr(B), r, float(alpha), X8.struct, _ptr(U),
                                   _ptr(dY), int(grad_format), _ptr(dX), _ptr(dA), _ptr(dB),
-                                  1 if accumulate else 0, _ptr(workspace), workspace.numel(),
-                                  _stream(stream)), "qlora_f8_linear_bwd")
+                                  1 if accumulate else 0, _ptr(workspace), workspace.numel(), s),
+        "qlora_f8_linear_bwd")
     if check:
         qlora_check(workspace, stream)
     return dX, dA, dB
