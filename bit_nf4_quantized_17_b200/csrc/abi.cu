@@ -487,7 +487,7 @@ qlora_status qlora_linear_bwd_f8_workspace(int64_t M, int64_t N, int64_t K, int3
   size_t bwd = 0;
   const qlora_status st = qlora_linear_workspace(M, N, K, r, nullptr, &bwd);
   if (st != QLORA_OK) return st;
-  if (bytes) *bytes = align256(bwd) + f8_input_bytes(M, K);
+  if (bytes) *bytes = align256(bwd) + f8_input_bytes(M, N, K, r);
   return QLORA_OK;
 }
 
@@ -517,7 +517,7 @@ qlora_status qlora_linear_bwd_f8(const qlora_nf4* W, const void* A, const void* 
   if ((st = check_linear(W, A, B, rt, M, workspace, workspace, workspace_bytes, true)) != QLORA_OK)
     return st;
   const size_t base = align256(plan_linear(M, W->rows, W->cols, rt).bwd_workspace);
-  if (workspace_bytes < base + f8_input_bytes(M, W->cols)) return QLORA_ERR_WORKSPACE;
+  if (workspace_bytes < base + f8_input_bytes(M, W->rows, W->cols, rt)) return QLORA_ERR_WORKSPACE;
   if (!dA || !dB || (M > 0 && (!U || !dY))) return QLORA_ERR_NULL;
   if (!aligned16(dY) || !aligned16(dA) || !aligned16(dB) || !aligned16(dX) || !aligned16(U))
     return QLORA_ERR_ALIGN;  // (a NULL dX counts as aligned)

@@ -34,4 +34,13 @@ struct F8Lora {
 qlora_status f8_gemm(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,
                      const F8Lora& lora, cudaStream_t s);
 
+// f8_grad.cu: dA (r x d_in fp32) = sc V^T X^ from X kept by rows in 8 bits (added to
+// dA when accumulate).  More than 16 tokens: V^T as bf16 hi rows [0, r) and lo
+// rows from lora_rows(r) on, ld_v elements a row; r a multiple of 8 up to 256.  Up
+// to 16 tokens: V (M x r fp32), r and d_in multiples of 8.
+qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t r, float sc,
+                       bool accumulate, float* dA, DeviceStatus* st, cudaStream_t s);
+qlora_status f8_small_grad_a(const float* V, const qlora_f8& x, int r, float sc, bool accumulate,
+                             float* dA, cudaStream_t s);
+
 }  // namespace qlora

@@ -1,0 +1,400 @@
+// dA = s V^T X^ from an input X that was kept in 8 bits (by rows): the one product
+// of the backward pass that reads X.
+//
+//   dA[j][k] = s sum_m V[m][j] X^[m][k],   X^[m][k] = bf16(code[m][k] scale[k / 128][m])
+//
+// It is bound by the read of the codes, one byte per element of X.  The scale
+// changes along the contraction (m), so it has to be applied to an operand: the
+// codes are expanded to bf16 on their way into the tensor core's operand tiles,
+// as the restored activations would be, and no bf16 copy of X is written.
+//
+// More than 16 tokens: D = X^T V^T per 128 columns of X on the tensor cores
+// (tcgen05.mma kind::f16, M = 128, N = 2 rc), V in bf16 as hi + lo (accurate to about
+// 2^-17; rank chunks of rc <= 128), the contraction split over a cluster and
+// summed in distributed shared memory in split order, as in gemm_rank.cu.  Roles (384
+// threads): warp 0 loads codes, warp 2 loads V^T, warp 1 owns TMEM and issues
+// the MMAs, warps 4-11 expand in two groups (group g takes 64-token tiles
+// i % 2 == g), warps 4-7 drain.  Every wait is bounded; a wait that gives up
+// reports QLORA_ERR_DEVICE_TIMEOUT.
+// Up to 16 tokens: CUDA cores, bound by writing dA; a thread takes 16 columns of 4
+// ranks, so that each code is expanded once for 4 ranks.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
+#include "f8.cuh"
+#include "tc_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace qlora {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kABytes = 16384;     // 64 tokens x 128 columns in bf16, two 64-column halves
+constexpr int kCodeBytes = 8192;   // 64 tokens x 128 codes
+constexpr int kCodeSlots = 4;
+constexpr int kStages = 2;
+constexpr long long kTimeoutCycles = 4000000000ll;
+
+struct GradArgs {
+  const float* scales;   // [kb][m]
+  int32_t m, k;          // tokens, columns of X
+  int32_t kt_total, kt_per;  // 64-token tiles, tiles per split
+  int32_t r, rc, lo_row;     // rank, ranks per chunk (a multiple of 16), first lo row of V^T
+  int32_t area;          // bytes of the tiles (the partial sums reuse them)
+  int32_t tmem_cols;
+  float* dA;
+  float sc;
+  int32_t accumulate;
+  uint32_t idesc;
+  DeviceStatus* st;
+};
+
+// 4 codes times a scale as 4 bf16
+template <bool E5M2>
+__device__ __forceinline__ uint2 expand4(uint32_t c, float s) {
+  constexpr __nv_fp8_interpretation_t kF = E5M2 ? __NV_E5M2 : __NV_E4M3;
+  const float2 a = __half22float2(__half2(
+      __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xffffu), kF)));
+  const float2 b = __half22float2(
+      __half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c >> 16), kF)));
+  return make_uint2(tc::pack_bf16x2(__fmul_rn(a.x, s), __fmul_rn(a.y, s)),
+                    tc::pack_bf16x2(__fmul_rn(b.x, s), __fmul_rn(b.y, s)));
+}
+
+template <bool E5M2>
+__global__ void __launch_bounds__(kThreads, 2)
+f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmV,
+               const GradArgs p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  // [kStages x (A | V^T)] [codes], reused as the fp32 partial sums
+  const int stage_bytes = kABytes + 2 * p.rc * 128;
+  uint8_t* codes = smem + kStages * stage_bytes;
+  float* red = reinterpret_cast<float*>(smem);  // [2 rc][132]: 128 columns of X each
+  constexpr int kRedLd = 132;
+  uint64_t* code_full = reinterpret_cast<uint64_t*>(smem + p.area);
+  uint64_t* code_empty = code_full + kCodeSlots;
+  uint64_t* full_a = code_empty + kCodeSlots;
+  uint64_t* full_b = full_a + kStages;
+  uint64_t* empty = full_b + kStages;
+  uint64_t* accum = empty + kStages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accum + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t S = gridDim.z, z = blockIdx.z;
+  const int kb = blockIdx.x, k0 = kb * 128;
+  const int j0 = blockIdx.y * p.rc;  // first rank of the chunk
+  const int t0 = static_cast<int>(z) * p.kt_per;
+  const int tn = max(0, min(p.kt_per, p.kt_total - t0));
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kCodeSlots; ++s) {
+      ptx::mbar_init(&code_full[s], 1);
+      ptx::mbar_init(&code_empty[s], 4);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      ptx::mbar_init(&full_a[s], 4);
+      ptx::mbar_init(&full_b[s], 1);
+      ptx::mbar_init(&empty[s], 1);
+    }
+    ptx::mbar_init(accum, 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+    ptx::prefetch_tmap(&tmX);
+    ptx::prefetch_tmap(&tmV);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(tmem_slot, p.tmem_cols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0 && ptx::elect_one()) {
+    // ------------------------------------------------------ codes
+    int issued = 0;
+    for (int i = 0; i < tn; ++i) {
+      const int s = i % kCodeSlots;
+      if (!ptx::mbar_wait(&code_empty[s], ((i / kCodeSlots) & 1) ^ 1, kTimeoutCycles, abort_flag))
+        break;
+      ptx::mbar_arrive_expect_tx(&code_full[s], kCodeBytes);
+      ptx::tma_load_2d(&tmX, &code_full[s], codes + s * kCodeBytes, k0, (t0 + i) * 64);
+      ++issued;
+    }
+    // never leave with copies in flight into this CTA's shared memory
+    for (int i = (issued > kCodeSlots ? issued - kCodeSlots : 0); i < issued; ++i)
+      ptx::mbar_wait(&code_full[i % kCodeSlots], (i / kCodeSlots) & 1, kTimeoutCycles, nullptr);
+  } else if (warp == 2 && ptx::elect_one()) {
+    // ------------------------------------------------------ V^T: hi and lo rows of the chunk
+    int issued = 0;
+    for (int i = 0; i < tn; ++i) {
+      const int s = i % kStages;
+      if (!ptx::mbar_wait(&empty[s], ((i / kStages) & 1) ^ 1, kTimeoutCycles, abort_flag)) break;
+      uint8_t* sv = smem + s * stage_bytes + kABytes;
+      ptx::mbar_arrive_expect_tx(&full_b[s], 2 * p.rc * 128);
+      ptx::tma_load_2d(&tmV, &full_b[s], sv, (t0 + i) * 64, j0);
+      ptx::tma_load_2d(&tmV, &full_b[s], sv + p.rc * 128, (t0 + i) * 64, p.lo_row + j0);
+      ++issued;
+    }
+    for (int i = (issued > kStages ? issued - kStages : 0); i < issued; ++i)
+      ptx::mbar_wait(&full_b[i % kStages], (i / kStages) & 1, kTimeoutCycles, nullptr);
+  } else if (warp == 1 && ptx::elect_one()) {
+    // ------------------------------------------------------ MMA issuer
+    for (int i = 0; i < tn; ++i) {
+      const int s = i % kStages;
+      const uint32_t ph = (i / kStages) & 1;
+      if (!ptx::mbar_wait(&full_b[s], ph, kTimeoutCycles, abort_flag) ||
+          !ptx::mbar_wait(&full_a[s], ph, kTimeoutCycles, abort_flag))
+        break;
+      ptx::tc_fence_after();
+      const uint32_t a_addr = ptx::smem_u32(smem + s * stage_bytes);
+      // A: MN-major, two 64-column halves 8192 bytes apart, 16 tokens (2048 bytes) a step
+      const uint64_t ad = ptx::sw128_desc(a_addr, 8192, 1024);
+      const uint64_t bd = ptx::sw128_desc(a_addr + kABytes, 16, 1024);
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        ptx::umma_bf16(tmem, ad + ((2048 * ks) >> 4), bd + ((32 * ks) >> 4), p.idesc,
+                       (i | ks) != 0 ? 1u : 0u);
+      ptx::umma_commit(&empty[s]);
+    }
+    ptx::umma_commit(accum);
+    ptx::mbar_wait(accum, 0, kTimeoutCycles, nullptr);  // MMAs done before TMEM is freed
+  } else if (warp >= 4) {
+    // ------------------------------------------------------ expansion
+    const int grp = (warp - 4) >> 2, td = (threadIdx.x - 128) & 127;
+    const int row = td & 63, h = td >> 6;  // token of the tile, half of its 128 columns
+    const float* sx = p.scales + static_cast<int64_t>(kb) * p.m;
+    auto scale_at = [&](int i) -> float {  // clamped: codes past the last token are zero
+      return __ldg(sx + min((t0 + i) * 64 + row, p.m - 1));
+    };
+    float next = grp < tn ? scale_at(grp) : 0.0f;
+    for (int i = grp; i < tn; i += 2) {
+      const int s = i % kCodeSlots, st = i % kStages;
+      if (!ptx::mbar_wait(&code_full[s], (i / kCodeSlots) & 1, kTimeoutCycles, abort_flag)) break;
+      const uint8_t* src = codes + s * kCodeBytes + row * 128;
+      uint4 c[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        c[q] = *reinterpret_cast<const uint4*>(src + 16 * ((4 * h + q) ^ (row & 7)));
+      const float sc = next;
+      if (i + 2 < tn) next = scale_at(i + 2);
+      // the next copy into the slot writes through the async proxy: order these
+      // reads before it, then release the slot
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&code_empty[s]);
+      uint4 o[8];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint2 e0 = expand4<E5M2>(c[q].x, sc), e1 = expand4<E5M2>(c[q].y, sc);
+        const uint2 e2 = expand4<E5M2>(c[q].z, sc), e3 = expand4<E5M2>(c[q].w, sc);
+        o[2 * q] = make_uint4(e0.x, e0.y, e1.x, e1.y);
+        o[2 * q + 1] = make_uint4(e2.x, e2.y, e3.x, e3.y);
+      }
+      if (!ptx::mbar_wait(&empty[st], ((i / kStages) & 1) ^ 1, kTimeoutCycles, abort_flag)) break;
+      uint8_t* dst = smem + st * stage_bytes + h * 8192 + row * 128;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(dst + 16 * (j ^ (row & 7))) = o[j];
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&full_a[st]);
+    }
+  }
+  __syncthreads();
+  // ---------------------------------------- partial sums to shared memory, transposed
+  if (warp >= 4 && warp < 8) {
+    const int i = 32 * (warp & 3) + lane;  // column of X in the tile
+    bool ok = tn > 0 && ptx::mbar_wait(accum, 0, kTimeoutCycles, abort_flag);
+    ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+    if (ok) ptx::tc_fence_after();
+    for (int c = 0; c < 2 * p.rc; c += 16) {
+      uint32_t r[16];
+      if (ok) {
+        ptx::tmem_ld_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, r);
+        ptx::tmem_ld_wait(r);
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+        red[(c + j) * kRedLd + i] = ok ? __uint_as_float(r[j]) : 0.0f;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();
+  // ---------------------------------------- hi + lo over the splits, in order
+  const int cols = min(p.rc, p.r - j0);
+  for (int e = static_cast<int>(z) * kThreads + threadIdx.x; e < cols * 128;
+       e += static_cast<int>(S) * kThreads) {
+    const int j = e >> 7, i = e & 127;
+    if (k0 + i >= p.k) continue;
+    float v = 0.0f;
+#pragma unroll
+    for (uint32_t q = 0; q < 8; ++q) {
+      if (q < S) {
+        const uint32_t at = ptx::cluster_addr(red, q) + 4u * (j * kRedLd + i);
+        v += ptx::ld_cluster_f32(at) + ptx::ld_cluster_f32(at + 4u * p.rc * kRedLd);
+      }
+    }
+    float* dst = p.dA + static_cast<int64_t>(j0 + j) * p.k + k0 + i;
+    *dst = p.accumulate ? *dst + p.sc * v : p.sc * v;
+  }
+  // no CTA leaves (or frees TMEM) while the others may still read its sums
+  __syncthreads();
+  ptx::cluster_sync();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, p.tmem_cols);
+  }
+  if (threadIdx.x == 0 && *abort_flag) report(p.st, QLORA_ERR_DEVICE_TIMEOUT, 140u);
+}
+
+// ------------------------------------------------------------ up to 16 tokens
+template <int MM, bool E5M2>
+__global__ void __launch_bounds__(128)
+f8_grad_small_kernel(const uint8_t* __restrict__ codes, const float* __restrict__ scales,
+                     int64_t ld, int M, int K, const float* __restrict__ V, int r, float sc,
+                     int accumulate, float* __restrict__ dA) {
+  const int k16 = (K + 15) / 16;
+  const int e = blockIdx.x * 128 + threadIdx.x;
+  if (e >= k16) return;
+  const int k = 16 * e, j = 4 * blockIdx.y;  // 16 columns, 4 ranks
+  const float* sx = scales + static_cast<int64_t>(k >> 7) * M;
+  float acc[4][16];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[q][i] = 0.0f;
+#pragma unroll
+  for (int m = 0; m < MM; ++m) {
+    if (m >= M) break;
+    const uint4 c = __ldg(reinterpret_cast<const uint4*>(codes + m * ld + k));
+    const float s = __ldg(sx + m);
+    const float4 v = __ldg(reinterpret_cast<const float4*>(V + m * r + j));
+    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint2 b = expand4<E5M2>(w[q], s);
+      const float x[4] = {__uint_as_float(b.x << 16), __uint_as_float(b.x & 0xffff0000u),
+                          __uint_as_float(b.y << 16), __uint_as_float(b.y & 0xffff0000u)};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[0][4 * q + i] = fmaf(v.x, x[i], acc[0][4 * q + i]);
+        acc[1][4 * q + i] = fmaf(v.y, x[i], acc[1][4 * q + i]);
+        acc[2][4 * q + i] = fmaf(v.z, x[i], acc[2][4 * q + i]);
+        acc[3][4 * q + i] = fmaf(v.w, x[i], acc[3][4 * q + i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float* dst = dA + static_cast<int64_t>(j + q) * K + k;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      if (k + i >= K) continue;  // K is a multiple of 8
+      float4 o = make_float4(sc * acc[q][i], sc * acc[q][i + 1], sc * acc[q][i + 2],
+                             sc * acc[q][i + 3]);
+      if (accumulate) {
+        const float4 d = *reinterpret_cast<const float4*>(dst + i);
+        o = make_float4(d.x + o.x, d.y + o.y, d.z + o.z, d.w + o.w);
+      }
+      *reinterpret_cast<float4*>(dst + i) = o;
+    }
+  }
+}
+
+template <int MM>
+void launch_small(const qlora_f8& x, const float* V, int r, float sc, int acc, float* dA,
+                  cudaStream_t s) {
+  const int K = static_cast<int>(x.cols), M = static_cast<int>(x.rows);
+  const dim3 grid(static_cast<unsigned>(ceil_div(ceil_div(K, 16), 128)), r / 4);
+  if (x.format == QLORA_E5M2)
+    f8_grad_small_kernel<MM, true><<<grid, 128, 0, s>>>(x.codes, x.scales, x.ld, M, K, V, r, sc,
+                                                        acc, dA);
+  else
+    f8_grad_small_kernel<MM, false><<<grid, 128, 0, s>>>(x.codes, x.scales, x.ld, M, K, V, r, sc,
+                                                         acc, dA);
+}
+
+}  // namespace
+
+qlora_status f8_small_grad_a(const float* V, const qlora_f8& x, int r, float sc, bool accumulate,
+                             float* dA, cudaStream_t s) {
+  if (x.rows < 1 || x.rows > kSmallM || x.cols % 8 != 0 || r % 8 != 0) return QLORA_ERR_UNSUPPORTED;
+  const int acc = accumulate ? 1 : 0;
+  count_launch();
+  if (x.rows == 1) launch_small<1>(x, V, r, sc, acc, dA, s);
+  else if (x.rows <= 4) launch_small<4>(x, V, r, sc, acc, dA, s);
+  else launch_small<16>(x, V, r, sc, acc, dA, s);
+  return after_launch("f8_small_grad_a", s);
+}
+
+qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t r, float sc,
+                       bool accumulate, float* dA, DeviceStatus* st, cudaStream_t s) {
+  const int64_t M = x.rows, K = x.cols;
+  const int32_t r16 = lora_rows(r);
+  GradArgs p{};
+  const int chunks = r16 > 128 ? 2 : 1;
+  p.rc = static_cast<int32_t>(ceil_div(r16, 16 * chunks) * 16);
+  CUtensorMap mx, mv;
+  if (!make_map(&mx, x.codes, false, K, M, x.ld, 128, 64, true) ||
+      !make_map(&mv, vt, true, M, r16 + r, ld_v, 64, static_cast<uint32_t>(p.rc), true))
+    return QLORA_ERR_CUDA;
+  p.scales = x.scales;
+  p.m = static_cast<int32_t>(M);
+  p.k = static_cast<int32_t>(K);
+  p.kt_total = static_cast<int32_t>(ceil_div(M, 64));
+  p.r = r;
+  p.lo_row = r16;
+  p.area = std::max(kStages * (kABytes + 2 * p.rc * 128) + kCodeSlots * kCodeBytes,
+                    2 * p.rc * 132 * 4);
+  p.tmem_cols = 32;
+  while (p.tmem_cols < 2 * p.rc) p.tmem_cols *= 2;
+  p.dA = dA;
+  p.sc = sc;
+  p.accumulate = accumulate ? 1 : 0;
+  p.idesc = ptx::idesc_bf16(128, 2 * p.rc, 1, 0);
+  p.st = st;
+  const bool e5 = x.format == QLORA_E5M2;
+  auto* fn = e5 ? f8_grad_kernel<true> : f8_grad_kernel<false>;
+  const size_t smem = 1024 + static_cast<size_t>(p.area) + 256;
+  const qlora_status cs = ensure_smem(reinterpret_cast<const void*>(fn), 200 * 1024);
+  if (cs != QLORA_OK) return cs;
+  const int64_t tiles = ceil_div(K, 128);
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    (void)cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  // splits of the tokens: as many CTAs as run at once (two per SM where the
+  // shared memory allows), at least 4 tiles each
+  const int64_t slots = (smem <= 112 * 1024 ? 2 : 1) * sms;
+  const int64_t want = std::min<int64_t>({8, slots / (tiles * chunks), p.kt_total / 4});
+  const int splits = static_cast<int>(std::max<int64_t>(1, want));
+  p.kt_per = static_cast<int32_t>(ceil_div(p.kt_total, splits));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles), chunks, splits);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  timing_mark(QLORA_KERNEL_LORA_GEMM, s, true);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, mx, mv, p);
+  timing_mark(QLORA_KERNEL_LORA_GEMM, s, false);
+  if (e != cudaSuccess) {
+    (void)cudaGetLastError();
+    return QLORA_ERR_CUDA;
+  }
+  return after_launch("f8_grad_a", s);
+}
+
+}  // namespace qlora

@@ -20,15 +20,15 @@ namespace {
 // Workspace (byte offsets; the status word is first).
 //   forward   sU [hi | lo]
 //   backward  sV [hi | lo] | V (fp32, few tokens) or V^T [hi ; lo] | U^T [hi ; lo] |
-//             dY codes | dY scales | split-K partials (ranks above 128) | X^ in bf16
+//             dY codes | dY scales | split-K partials of dB (ranks above 128)
 struct Layout {
   size_t su, fwd_end;
-  size_t sv, vt, ut, dy_codes, dy_scales, part, x_buf, bwd_end;
+  size_t sv, vt, ut, dy_codes, dy_scales, part, bwd_end;
   int64_t dy_ld;
-  int split_db, split_da;
+  int split_db;
 };
 
-Layout layout(int64_t M, int64_t N, int64_t K, int32_t r) {
+Layout layout(int64_t M, int64_t N, int32_t r) {
   Layout L{};
   if (M < 1) M = 1;  // no tokens: no work, but a workspace with a status word
   const int64_t span = lora_span(r), r16 = lora_rows(r), mp = pad8(M);
@@ -42,19 +42,16 @@ Layout layout(int64_t M, int64_t N, int64_t K, int32_t r) {
   L.dy_scales = L.dy_codes + align256(M * L.dy_ld);
   L.part = L.dy_scales + align256(sizeof(float) * f8_blocks(N) * M);
   L.split_db = tc_split_count(ceil_div(N, 128), ceil_div(M, 64));
-  L.split_da = tc_split_count(ceil_div(K, 128), ceil_div(M, 64));
   const bool one_launch = 2 * r16 <= 256;
-  L.x_buf = L.part + (one_launch ? 0
-                                 : align256(sizeof(float) * 2 * r16 *
-                                            std::max(L.split_db * N, L.split_da * K)));
-  L.bwd_end = L.x_buf + f8_input_bytes(M, K);
+  L.bwd_end = L.part + (one_launch ? 0 : align256(sizeof(float) * 2 * r16 * L.split_db * N));
   return L;
 }
 
 }  // namespace
 
 LinearPlan plan_f8_linear(int64_t M, int64_t N, int64_t K, int32_t r) {
-  const Layout L = layout(M, N, K, r);
+  (void)K;
+  const Layout L = layout(M, N, r);
   return LinearPlan{L.fwd_end, L.bwd_end};
 }
 
@@ -62,7 +59,7 @@ qlora_status f8_linear_forward(const qlora_f8& W, const void* A, const void* B, 
                                float alpha, const void* X, const qlora_f8& x8, void* Y,
                                float* U_save, void* workspace, cudaStream_t s) {
   const int64_t M = x8.rows, N = W.rows, K = W.cols;
-  const Layout L = layout(M, N, K, r);
+  const Layout L = layout(M, N, r);
   const float sc = lora_scale(alpha, r);
   const int32_t r16 = lora_rows(r), span = lora_span(r);
   char* ws = static_cast<char*>(workspace);
@@ -94,7 +91,7 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
                                 int32_t grad_format, void* dX, float* dA, float* dB,
                                 bool accumulate, void* workspace, cudaStream_t s) {
   const int64_t M = x8.rows, N = W.rows, K = W.cols;
-  const Layout L = layout(M, N, K, r);
+  const Layout L = layout(M, N, r);
   const float sc = lora_scale(alpha, r);
   const int32_t r16 = lora_rows(r), span = lora_span(r);
   const int64_t mp = pad8(M);
@@ -103,7 +100,6 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
   char *sv = ws + L.sv, *vt = ws + L.vt, *ut = ws + L.ut;
   float* v = reinterpret_cast<float*>(vt);  // few tokens: V in fp32
   float* part = reinterpret_cast<float*>(ws + L.part);
-  void* xb = ws + L.x_buf;
   const bool small = M <= kSmallM;
   // V = dY B -> sV = s V as [hi | lo], and V (fp32) or V^T as [hi ; lo]
   if (small) {
@@ -139,11 +135,10 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
     return f8_gemm(dy8, W, false, dX, false, F8Lora{sv, A, r}, s);
   };
   auto side_work = [&]() -> qlora_status {
-    QLORA_TRY(launch_f8_dequantize(x8, xb, QLORA_BF16, s2));
     if (small) {
       const int m = static_cast<int>(M);
       QLORA_TRY(small_grad_b(dY, U, m, N, r, sc, accumulate, dB, s2));
-      return small_grad_a(v, xb, m, K, r, sc, accumulate, dA, s2);
+      return f8_small_grad_a(v, x8, r, sc, accumulate, dA, s2);
     }
     QLORA_TRY(transpose_to_bf16(U, true, M, r, r, ut, mp, r16, s2));
     ReduceArgs rb = reduce_args(part, L.split_db, N, r, 2 * r16);
@@ -154,15 +149,7 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
     rb.acc1 = accumulate;
     QLORA_TRY(rank_product(dY, true, N, M, N, ut, mp, 2 * r16, 2 * r16, part, L.split_db, rb, st,
                            s2));
-    ReduceArgs ra = reduce_args(part, L.split_da, K, r, 2 * r16);
-    ra.lo = r16;
-    ra.o1 = dA;
-    ra.ld1 = K;
-    ra.trans1 = true;
-    ra.a1 = sc;
-    ra.acc1 = accumulate;
-    return rank_product(xb, true, K, M, K, vt, mp, 2 * r16, 2 * r16, part, L.split_da, ra, st,
-                        s2);
+    return f8_grad_a(vt, mp, x8, r, sc, accumulate, dA, st, s2);
   };
   const qlora_status st_main = main_work();
   const qlora_status st_side = side_work();

@@ -189,7 +189,9 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, int32_t r) {
   return p;
 }
 
-size_t f8_input_bytes(int64_t M, int64_t K) { return align256(2 * M * K); }
+size_t f8_input_bytes(int64_t M, int64_t N, int64_t K, int32_t r) {
+  return use_tc(M, N, K, r) ? 0 : align256(2 * M * K);
+}
 
 bool linear_multi_supported(int64_t M, int64_t N, int64_t K, int32_t r) {
   return use_tc(M > 0 ? M : 1, N, K, r);  // (M = 0 is a no-op on every path)
@@ -345,7 +347,7 @@ qlora_status linear_backward(const qlora_nf4& W, const LevelTable& t, const void
     };
     auto side_work = [&]() -> qlora_status {
       QLORA_TRY(small_grad_b(dY, U, m, N, r, sc, accumulate, dB, s2));
-      if (o.x8) QLORA_TRY(launch_f8_dequantize(*o.x8, o.x_buf, QLORA_BF16, s2));
+      if (o.x8) return f8_small_grad_a(v, *o.x8, r, sc * o.keep, accumulate, dA, s2);
       return small_grad_a(v, xl, m, K, r, sc * o.keep, accumulate, dA, s2);
     };
     // the dX kernel is enqueued first so that it takes the SMs
@@ -433,7 +435,7 @@ qlora_status linear_backward(const qlora_nf4& W, const LevelTable& t, const void
         QLORA_TRY(rank_product(dY, true, N, M, N, ut, mp, 2 * r16, 2 * r16, part, sp.db, ra, st,
                                s2));
       }
-      if (o.x8) QLORA_TRY(launch_f8_dequantize(*o.x8, o.x_buf, QLORA_BF16, s2));
+      if (o.x8) return f8_grad_a(vt, mp, *o.x8, r, sc * o.keep, accumulate, dA, st, s2);
       // dA = s V^T X: rows d_in, stored transposed as r x d_in
       ReduceArgs ra = reduce_args(part, sp.da, K, r, 2 * r16);
       ra.lo = r16;

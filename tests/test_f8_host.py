@@ -151,7 +151,10 @@ def test_workspace_queries():
         f, b = Q.qlora_f8_linear_workspace(M, 256, 128, 16)
         assert 256 <= f <= b
         assert Q.qlora_linear_bwd_f8_workspace(M, 256, 128, 16) >= \
-            Q.qlora_linear_workspace(M, 256, 128, 16)[1] + 2 * M * 128
+            Q.qlora_linear_workspace(M, 256, 128, 16)[1]
+        # a rank that the CUDA-core path takes: X restored in bf16
+        assert Q.qlora_linear_bwd_f8_workspace(M, 256, 128, 5) >= \
+            Q.qlora_linear_workspace(M, 256, 128, 5)[1] + 2 * M * 128
     for args in ((-1, 8, 8, 8), (1, 0, 8, 8), (1, 8, 8, 257), (1 << 30, 8, 8, 8)):
         with pytest.raises(Q.QloraError) as e:
             Q.qlora_f8_linear_workspace(*args)
