@@ -37,11 +37,12 @@ using f8::store_run;
 constexpr int kEpi = 8;
 constexpr int kRoleWarps = 4;                // TMA, MMA, scales, one idle
 constexpr int kThreads = 32 * (kRoleWarps + kEpi);
-constexpr int kStages = 6;
+constexpr int kStages = 5;
 constexpr int kOpBytes = 16384;              // 128 rows x 128 bytes: A, and this CTA's half of B
 constexpr int kStageBytes = 2 * kOpBytes;
 using Ring = f8::ScaleRing<128, 2>;
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + sizeof(Ring) + 256;
+constexpr int kOutBytes = 4096;              // a warp's part of C on its way: 32 rows x 128 bytes
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpi * kOutBytes + sizeof(Ring) + 256;
 constexpr int kGroup = 16;                   // row tiles per column tile before the next one
 
 __device__ __forceinline__ void tile_at(const GemmArgs& p, int m_tiles, int t, int* mt, int* nt) {
@@ -55,11 +56,12 @@ __device__ __forceinline__ void tile_at(const GemmArgs& p, int m_tiles, int t, i
 __global__ void __launch_bounds__(kThreads, 1)
 f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const __grid_constant__ CUtensorMap tmL, const __grid_constant__ CUtensorMap tmR,
-               const GemmArgs p) {
+               const __grid_constant__ CUtensorMap tmC, const GemmArgs p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  Ring* ring = reinterpret_cast<Ring*>(smem + kStages * kStageBytes);
+  uint8_t* out_stage = smem + kStages * kStageBytes;
+  Ring* ring = reinterpret_cast<Ring*>(out_stage + kEpi * kOutBytes);
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + 1);  // even CTA's count
   uint64_t* empty = full + kStages;
   uint64_t* acc_full = empty + kStages;
@@ -341,19 +343,67 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       }
       if (p.ext_tiles && ok) add_block(1.0f, 1.0f, []() {});  // the LoRA term
       ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-      const int row = mt * 256 + static_cast<int>(rank) * 128 + lrow;
-      const int col = nt * 256 + 64 * h;
+      const int row0 = mt * 256 + static_cast<int>(rank) * 128 + 32 * quarter;
+      const int col0 = nt * 256 + 64 * h;
+      // value j of the thread's row: column col0 + j, or col0 + 64 + j from 64 on
+      auto value = [&](int j) -> float {
+        float lo, hi;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(acc[j / 2]));
+        return ok ? (j & 1 ? hi : lo) : __int_as_float(0x7fffffff);
+      };
+      if (p.c_tma) {
+        // through shared memory, 128 bytes of each row at a time: the copy engine
+        // writes whole lines while the next tile is multiplied (stores from the
+        // registers, 16 bytes of 32 rows an instruction, took 2 us a tile)
+        uint8_t* stage = out_stage + (warp - kRoleWarps) * kOutBytes;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        float v[16];
+        for (int c = 0; c < 4; ++c) {       // 32 columns
+          const bool first = p.c_f32 || (c & 1) == 0;
+          if (first) {
+            if (lane == 0) ptx::bulk_wait_read();
+            __syncwarp();
+          }
+          if (p.c_f32) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * j]), "=f"(v[2 * j + 1]) : "l"(acc[8 * c + j]));
-          if (!ok) v[2 * j] = v[2 * j + 1] = __int_as_float(0x7fffffff);
+            for (int q = 0; q < 8; ++q)
+              *reinterpret_cast<float4*>(stage + lane * 128 + 16 * (q ^ (lane & 7))) =
+                  make_float4(value(32 * c + 4 * q), value(32 * c + 4 * q + 1),
+                              value(32 * c + 4 * q + 2), value(32 * c + 4 * q + 3));
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                w[j] = tc::pack_bf16x2(value(32 * c + 8 * q + 2 * j),
+                                       value(32 * c + 8 * q + 2 * j + 1));
+              *reinterpret_cast<uint4*>(stage + lane * 128 +
+                                        16 * ((4 * (c & 1) + q) ^ (lane & 7))) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          if (p.c_f32 || (c & 1)) {
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            const int col = col0 + 128 * (c >> 1) + (p.c_f32 ? 32 * (c & 1) : 0);
+            if (lane == 0 && row0 < p.m && col < p.n) {
+              // (an fp32 C is described as pairs of 16-bit columns)
+              ptx::tma_store_2d(&tmC, stage, p.c_f32 ? 2 * col : col, row0);
+              ptx::bulk_commit();
+            }
+          }
         }
-        store_run<16>(p, row, col + 128 * (c >> 2) + 16 * (c & 3), v);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          float v[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = value(16 * c + j);
+          store_run<16>(p, row0 + lane, col0 + 128 * (c >> 2) + 16 * (c & 3), v);
+        }
       }
     }
+    if (lane == 0) ptx::bulk_wait_read();  // before shared memory goes
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -384,6 +434,11 @@ qlora_status f8_gemm_pairs(const qlora_f8& a, const qlora_f8& b, bool trans_b, v
     ml = ma;
     mr = mb;
   }
+  // C through TMA stores where its rows start on 16 bytes
+  const int64_t words = c_f32 ? 2 * n : n;
+  CUtensorMap mc = ma;
+  p.c_tma = words % 8 == 0 ? 1 : 0;
+  if (p.c_tma) ok = ok && make_map(&mc, c, true, words, m, words, 64, 32, true);
   if (!ok) return QLORA_ERR_CUDA;
   const int fa = a.format == QLORA_E5M2 ? 1 : 0, fb = b.format == QLORA_E5M2 ? 1 : 0;
   p.idesc = ptx::idesc_f8(fa, fb, 256, 128, 0, p.b_mn);
@@ -410,7 +465,7 @@ qlora_status f8_gemm_pairs(const qlora_f8& a, const qlora_f8& b, bool trans_b, v
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   count_launch();
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, f8_pair_kernel, ma, mb, ml, mr, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, f8_pair_kernel, ma, mb, ml, mr, mc, p);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return QLORA_ERR_CUDA;

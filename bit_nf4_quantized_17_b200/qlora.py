@@ -655,6 +655,15 @@ def qlora_f8_matmul(a, b, trans_b=True, dtype=torch.bfloat16, out=None, stream=N
     return out
 
 
+def _expect(name, t, shape, dtype):
+    """The check of _check_linear for one tensor."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of shape {shape}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
 def qlora_linear_bwd_f8_workspace(M, N, K, r):
     b = ctypes.c_size_t()
     _ok(lib().qlora_linear_bwd_f8_workspace(M, N, K, r, ctypes.byref(b)),
@@ -663,13 +672,18 @@ def qlora_linear_bwd_f8_workspace(M, N, K, r):
 
 
 def _grads(M, N, K, r, device, want_dx, dX, dA, dB, stream):
-    if want_dx and dX is None:
-        dX = _empty_in(stream, (M, K), torch.bfloat16, device)
+    """dX, dA, dB, allocated where they are not given, and their addresses."""
+    bf16, f32 = torch.bfloat16, torch.float32
+    if not want_dx:
+        dX = None
+    elif dX is None:
+        dX = _empty_in(stream, (M, K), bf16, device)
     if dA is None:
-        dA = _empty_in(stream, (r, K), torch.float32, device)
+        dA = _empty_in(stream, (r, K), f32, device)
     if dB is None:
-        dB = _empty_in(stream, (N, r), torch.float32, device)
-    return (dX if want_dx else None), dA, dB
+        dB = _empty_in(stream, (N, r), f32, device)
+    px = None if dX is None else _expect("dX", dX, (M, K), bf16)
+    return dX, dA, dB, px, _expect("dA", dA, (r, K), f32), _expect("dB", dB, (N, r), f32)
 
 
 def qlora_linear_bwd_f8(q, A, B, r, alpha, X8, U, dY, adapter=None, p=0.0, keep_mask=None,
@@ -683,19 +697,24 @@ def qlora_linear_bwd_f8(q, A, B, r, alpha, X8, U, dY, adapter=None, p=0.0, keep_
                          f"{'' if X8.layout == QLORA_F8_ROWS else ' held by tiles'}")
     if U is None:
         raise ValueError("U: the forward's X A^T is needed, X is not kept")
-    dX, dA, dB = _grads(M, q.rows, q.cols, rt, dev, want_dx, dX, dA, dB, stream)
-    o = _opts(r, A, adapter, p, keep_mask, None)
-    _check_linear(q, M, rt, A=A, B=B, U=U, dY=dY, dX=dX, dA=dA, dB=dB, adapter=adapter,
-                  keep_mask=keep_mask)
+    N, K, bf16, f32 = q.rows, q.cols, torch.bfloat16, torch.float32
+    pa, pb = _expect("A", A, (rt, K), bf16), _expect("B", B, (N, rt), bf16)
+    pu, py = _expect("U", U, (M, rt), f32), _expect("dY", dY, (M, N), bf16)
+    if adapter is not None:
+        _expect("adapter", adapter, (M,), torch.int32)
+    if keep_mask is not None:
+        _expect("keep_mask", keep_mask, (M, K // 8), torch.uint8)
+    o = None
+    if adapter is not None or keep_mask is not None or rt != r:
+        o = _opts(r, A, adapter, p, keep_mask, None)
+    dX, dA, dB, px, pda, pdb = _grads(M, N, K, rt, dev, want_dx, dX, dA, dB, stream)
     s = _device_stream(stream, q.codes, X8.codes, A, B, U, dY, dX, dA, dB, adapter, keep_mask,
                        workspace)
     if workspace is None:
-        workspace = _workspace_in(stream, qlora_linear_bwd_f8_workspace(M, q.rows, q.cols, rt),
-                                  dev)
-    _ok(lib().qlora_linear_bwd_f8(q.struct, _ptr(A), _ptr(B), r, float(alpha), o, X8.struct,
-                                  _ptr(U), _ptr(dY), _ptr(dX), _ptr(dA), _ptr(dB),
-                                  1 if accumulate else 0, _ptr(workspace), workspace.numel(), s),
-        "qlora_linear_bwd_f8")
+        workspace = _workspace_in(stream, qlora_linear_bwd_f8_workspace(M, N, K, rt), dev)
+    _ok(lib().qlora_linear_bwd_f8(q.struct, pa, pb, r, float(alpha), o, X8.struct, pu, py, px, pda,
+                                  pdb, 1 if accumulate else 0, workspace.data_ptr(),
+                                  workspace.numel(), s), "qlora_linear_bwd_f8")
     if check:
         qlora_check(workspace, stream)
     return dX, dA, dB
@@ -721,17 +740,19 @@ def qlora_f8_linear_fwd(W, A, B, alpha, X, X8, Y=None, U_save=None, workspace=No
     """The linear layer over an 8-bit base W (an F8Matrix by tiles): Y = X^ W^T + (alpha/r)
     (X A^T) B^T.  X8 (an F8Matrix by rows, e.g. F8Matrix.empty(M, d_in)) receives the 8 bits
     of X and is what the backward takes.  Returns Y."""
-    M, r = X8.rows, A.shape[0]
+    M, r, N, K = X8.rows, A.shape[0], W.rows, W.cols
+    bf16 = torch.bfloat16
     _check_f8_base(W, X8)
     if Y is None:
-        Y = _empty_in(stream, (M, W.rows), torch.bfloat16, X.device)
-    _check_linear(W, M, r, A=A, B=B, X=X, Y=Y, U=U_save)
+        Y = _empty_in(stream, (M, N), bf16, X.device)
+    pa, pb = _expect("A", A, (r, K), bf16), _expect("B", B, (N, r), bf16)
+    px, py = _expect("X", X, (M, K), bf16), _expect("Y", Y, (M, N), bf16)
+    pu = None if U_save is None else _expect("U", U_save, (M, r), torch.float32)
     s = _device_stream(stream, W.codes, A, B, X, X8.codes, Y, U_save, workspace)
     if workspace is None:
-        workspace = _workspace_in(stream, qlora_f8_linear_workspace(M, W.rows, W.cols, r)[0],
-                                  X.device)
-    _ok(lib().qlora_f8_linear_fwd(W.struct, _ptr(A), _ptr(B), r, float(alpha), _ptr(X), X8.struct,
-                                  _ptr(Y), _ptr(U_save), _ptr(workspace), workspace.numel(), s),
+        workspace = _workspace_in(stream, qlora_f8_linear_workspace(M, N, K, r)[0], X.device)
+    _ok(lib().qlora_f8_linear_fwd(W.struct, pa, pb, r, float(alpha), px, X8.struct, py, pu,
+                                  workspace.data_ptr(), workspace.numel(), s),
         "qlora_f8_linear_fwd")
     if check:
         qlora_check(workspace, stream)
@@ -747,14 +768,16 @@ def qlora_f8_linear_bwd(W, A, B, alpha, X8, U, dY, grad_format=QLORA_E5M2, dX=No
     _check_f8_base(W, X8)
     if U is None:
         raise ValueError("U: the forward's X A^T is needed, X is not kept")
-    dX, dA, dB = _grads(M, W.rows, W.cols, r, dev, want_dx, dX, dA, dB, stream)
-    _check_linear(W, M, r, A=A, B=B, U=U, dY=dY, dX=dX, dA=dA, dB=dB)
+    N, K, bf16 = W.rows, W.cols, torch.bfloat16
+    pa, pb = _expect("A", A, (r, K), bf16), _expect("B", B, (N, r), bf16)
+    pu, py = _expect("U", U, (M, r), torch.float32), _expect("dY", dY, (M, N), bf16)
+    dX, dA, dB, px, pda, pdb = _grads(M, N, K, r, dev, want_dx, dX, dA, dB, stream)
     s = _device_stream(stream, W.codes, X8.codes, A, B, U, dY, dX, dA, dB, workspace)
     if workspace is None:
-        workspace = _workspace_in(stream, qlora_f8_linear_workspace(M, W.rows, W.cols, r)[1], dev)
-    _ok(lib().qlora_f8_linear_bwd(W.struct, _ptr(A), _ptr(B), r, float(alpha), X8.struct, _ptr(U),
-                                  _ptr(dY), int(grad_format), _ptr(dX), _ptr(dA), _ptr(dB),
-                                  1 if accumulate else 0, _ptr(workspace), workspace.numel(), s),
+        workspace = _workspace_in(stream, qlora_f8_linear_workspace(M, N, K, r)[1], dev)
+    _ok(lib().qlora_f8_linear_bwd(W.struct, pa, pb, r, float(alpha), X8.struct, pu, py,
+                                  int(grad_format), px, pda, pdb, 1 if accumulate else 0,
+                                  workspace.data_ptr(), workspace.numel(), s),
         "qlora_f8_linear_bwd")
     if check:
         qlora_check(workspace, stream)
