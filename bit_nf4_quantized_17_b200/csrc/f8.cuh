@@ -15,8 +15,11 @@ inline int64_t f8_blocks(int64_t n) { return ceil_div(n, 128); }
 // abi_f8.cu: shape and pointer checks of a qlora_f8.
 qlora_status check_f8(const qlora_f8& q);
 
-// f8_quantize.cu
-qlora_status launch_f8_quantize(const void* X, int32_t x_dtype, const qlora_f8& q, cudaStream_t s);
+// f8_quantize.cu.  beside_last: the launch may run beside the one before it in the
+// stream (a programmatic dependent launch that waits for nothing): only where that
+// one reads and writes none of q's arrays and does not write X.
+qlora_status launch_f8_quantize(const void* X, int32_t x_dtype, const qlora_f8& q, cudaStream_t s,
+                                bool beside_last = false);
 qlora_status launch_f8_dequantize(const qlora_f8& q, void* out, int32_t out_dtype,
                                   cudaStream_t s);
 

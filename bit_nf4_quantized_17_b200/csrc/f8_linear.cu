@@ -65,7 +65,6 @@ qlora_status f8_linear_forward(const qlora_f8& W, const void* A, const void* B, 
   char* ws = static_cast<char*>(workspace);
   auto* st = reinterpret_cast<DeviceStatus*>(ws);
   char* su = ws + L.su;
-  QLORA_TRY(launch_f8_quantize(X, QLORA_BF16, x8, s));
   // U = X A^T -> U_save (fp32) and sU = s U as bf16 hi + lo
   if (M <= kSmallM) {
     const RankOut ro{r, U_save, r, 1.0f, reinterpret_cast<__nv_bfloat16*>(su), 2 * span,
@@ -83,6 +82,8 @@ qlora_status f8_linear_forward(const qlora_f8& W, const void* A, const void* B, 
     ra.o2_pad = 1;
     QLORA_TRY(tc_rank_gemm(X, false, M, K, K, A, false, K, r, r16, ra, st, s));
   }
+  // beside the U launch, which starts when all work before it is done and shares only X
+  QLORA_TRY(launch_f8_quantize(X, QLORA_BF16, x8, s, true));
   return f8_gemm(x8, W, true, Y, false, F8Lora{su, B, r}, s);
 }
 
@@ -119,6 +120,11 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
     ra.o3_lo = r16;
     QLORA_TRY(tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s));
   }
+  const qlora_f8 dy8{M, N, L.dy_ld, QLORA_F8_ROWS, grad_format, x8.pow2, 0,
+                     reinterpret_cast<uint8_t*>(ws + L.dy_codes),
+                     reinterpret_cast<float*>(ws + L.dy_scales)};
+  // beside the V launch, which shares only dY
+  if (dX) QLORA_TRY(launch_f8_quantize(dY, QLORA_BF16, dy8, s, true));
   // dB and dA on the side stream, dX on the caller's: they share only inputs
   SideStream* ss = nullptr;
   QLORA_TRY(side_stream(&ss));
@@ -128,10 +134,6 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
     return QLORA_ERR_CUDA;
   auto main_work = [&]() -> qlora_status {
     if (!dX) return QLORA_OK;
-    const qlora_f8 dy8{M, N, L.dy_ld, QLORA_F8_ROWS, grad_format, x8.pow2, 0,
-                       reinterpret_cast<uint8_t*>(ws + L.dy_codes),
-                       reinterpret_cast<float*>(ws + L.dy_scales)};
-    QLORA_TRY(launch_f8_quantize(dY, QLORA_BF16, dy8, s));
     return f8_gemm(dy8, W, false, dX, false, F8Lora{sv, A, r}, s);
   };
   auto side_work = [&]() -> qlora_status {
