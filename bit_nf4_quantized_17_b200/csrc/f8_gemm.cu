@@ -142,6 +142,9 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
   // in them cost 600 and 1100 cycles a block, more than the block's bytes or MMAs.)
   if (warp == 0 && ptx::elect_one()) {
     // ------------------------------------------------------ TMA producer
+    // the launch may start before the one ahead of it is done: everything before
+    // this touched no memory of the caller's, everything after follows these loads
+    ptx::grid_dependency_wait();
     int s = 0, issued = 0;
     uint32_t ph = 1;
     bool go = true;
@@ -267,6 +270,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
     }
   } else if (warp == 2) {
     // ------------------------------------------------------ scales
+    ptx::grid_dependency_wait();
     for (int kb = 0, c = 0; kb < kn; kb += f8::kChunk, ++c) {
       bool go = ptx::mbar_wait(&sc_empty[c & 1], ((c >> 1) & 1) ^ 1, kTimeoutCycles, abort_flag);
       go = __all_sync(0xffffffffu, go);
@@ -483,13 +487,15 @@ qlora_status launch(const qlora_f8& a, const qlora_f8& b, bool trans_b, GemmArgs
   cfg.dynamicSmemBytes =
       1024 + std::max(p.stages * C::kStage, C::kRedBytes) + sizeof(typename C::Ring) + 512;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   count_launch();
   const cudaError_t e = cudaLaunchKernelEx(&cfg, f8_gemm_kernel<BN, SWAP>, SWAP ? mb : ma,
                                            SWAP ? ma : mb, SWAP ? mr : ml, SWAP ? ml : mr, p);

@@ -114,6 +114,9 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   ptx::setmaxnreg_dec<40>();
   if (warp == 0 && ptx::elect_one()) {
     // ------------------------------------------------------ TMA producer
+    // the launch may start before the one ahead of it is done: everything before
+    // this touched no memory of the caller's, everything after follows these loads
+    ptx::grid_dependency_wait();
     int it = 0, s = 0;
     uint32_t ph = 1;
     bool ok = true;
@@ -252,6 +255,7 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     ptx::mbar_wait(drain, 0, kTimeoutCycles, nullptr);
   } else if (warp == 2) {
     // ------------------------------------------------------ scales
+    ptx::grid_dependency_wait();
     int chunk = 0;
     bool ok = true;
     for (int t = pair; t < tiles && ok; t += pairs) {
@@ -457,13 +461,15 @@ qlora_status f8_gemm_pairs(const qlora_f8& a, const qlora_f8& b, bool trans_b, v
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.numAttrs = 2;
   count_launch();
   const cudaError_t e = cudaLaunchKernelEx(&cfg, f8_pair_kernel, ma, mb, ml, mr, mc, p);
   if (e != cudaSuccess) {

@@ -140,6 +140,13 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// ---------------------------------------------------------------- dependent launches
+// Wait until the launches this one depends on are done and their writes visible
+// (returns at once in a launch without the programmatic attribute).
+__device__ __forceinline__ void grid_dependency_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- registers
 // Hand registers from the warps of one warpgroup to those of another (all four
 // warps of a warpgroup execute it; the shares add up to what the launch has).
