@@ -8,9 +8,10 @@ using namespace qlora;
 namespace qlora {
 
 static constexpr int64_t kMaxElems = int64_t(1) << 36;
+static constexpr int64_t kMaxSide = int64_t(1) << 30;  // tile coordinates stay inside 32 bits
 
 static qlora_status check_f8_shape(int64_t rows, int64_t cols, int32_t layout) {
-  if (rows < 0 || cols < 1 || rows > 0x7fffffff || cols > 0x7fffff00) return QLORA_ERR_SHAPE;
+  if (rows < 0 || cols < 1 || rows > kMaxSide || cols > kMaxSide) return QLORA_ERR_SHAPE;
   if (rows > kMaxElems / cols) return QLORA_ERR_SHAPE;
   if (layout != QLORA_F8_ROWS && layout != QLORA_F8_TILES) return QLORA_ERR_UNSUPPORTED;
   return QLORA_OK;
@@ -91,8 +92,7 @@ qlora_status qlora_f8_matmul(const qlora_f8* A, const qlora_f8* B, int32_t trans
 
 qlora_status qlora_f8_linear_workspace(int64_t M, int64_t N, int64_t K, int32_t r,
                                        size_t* fwd_bytes, size_t* bwd_bytes) {
-  if (M < 0 || N < 1 || K < 1 || r < 1 || r > 256 || M > 0x3fffffff || N > 0x7fffffff ||
-      K > 0x7fffff00)
+  if (M < 0 || N < 1 || K < 1 || r < 1 || r > 256 || M > kMaxSide || N > kMaxSide || K > kMaxSide)
     return QLORA_ERR_SHAPE;
   const LinearPlan p = plan_f8_linear(M, N, K, r);
   if (fwd_bytes) *fwd_bytes = p.fwd_workspace;
@@ -108,8 +108,7 @@ static qlora_status check_f8_linear(const qlora_f8* W, const void* A, const void
   if (st != QLORA_OK) return st;
   if ((st = check_f8(*X8)) != QLORA_OK) return st;
   if (W->layout != QLORA_F8_TILES || X8->layout != QLORA_F8_ROWS) return QLORA_ERR_UNSUPPORTED;
-  if (W->rows < 1 || X8->cols != W->cols || r < 1 || r > 256 || X8->rows > 0x3fffffff)
-    return QLORA_ERR_SHAPE;
+  if (W->rows < 1 || X8->cols != W->cols || r < 1 || r > 256) return QLORA_ERR_SHAPE;
   // TMA reads bf16 rows of r, N and K elements: multiples of 16 bytes
   if (r % 8 != 0 || W->rows % 8 != 0 || W->cols % 8 != 0) return QLORA_ERR_UNSUPPORTED;
   if (!aligned16(A) || !aligned16(B) || !aligned16(workspace)) return QLORA_ERR_ALIGN;

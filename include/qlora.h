@@ -322,8 +322,8 @@ typedef struct {
 } qlora_f8;
 
 /* The smallest ld and the byte sizes of the arrays of a rows x cols matrix (any
- * output may be NULL).  QLORA_ERR_SHAPE for rows < 0, cols < 1, a side of 2^31 or
- * more, or more than 2^36 elements; QLORA_ERR_UNSUPPORTED for another layout. */
+ * output may be NULL).  QLORA_ERR_SHAPE for rows < 0, cols < 1, a side above
+ * 2^30, or more than 2^36 elements; QLORA_ERR_UNSUPPORTED for another layout. */
 qlora_status qlora_f8_sizes(int64_t rows, int64_t cols, int32_t layout, int64_t* ld,
                             size_t* codes_bytes, size_t* scales_bytes);
 

@@ -25,7 +25,8 @@ def test_sizes():
                                                             "scales": 16}
     assert Q.qlora_f8_sizes(0, 1, Q.QLORA_F8_ROWS) == {"ld": 16, "codes": 0, "scales": 0}
     for rows, cols, layout, st in ((-1, 8, 0, Q.QLORA_ERR_SHAPE), (8, 0, 0, Q.QLORA_ERR_SHAPE),
-                                   (1 << 31, 1, 0, Q.QLORA_ERR_SHAPE),
+                                   ((1 << 30) + 1, 1, 0, Q.QLORA_ERR_SHAPE),
+                                   (1, (1 << 30) + 1, 0, Q.QLORA_ERR_SHAPE),
                                    (1 << 20, 1 << 20, 0, Q.QLORA_ERR_SHAPE),
                                    (8, 8, 2, Q.QLORA_ERR_UNSUPPORTED)):
         with pytest.raises(Q.QloraError) as e:
@@ -155,7 +156,7 @@ def test_workspace_queries():
         # a rank that the CUDA-core path takes: X restored in bf16
         assert Q.qlora_linear_bwd_f8_workspace(M, 256, 128, 5) >= \
             Q.qlora_linear_workspace(M, 256, 128, 5)[1] + 2 * M * 128
-    for args in ((-1, 8, 8, 8), (1, 0, 8, 8), (1, 8, 8, 257), (1 << 30, 8, 8, 8)):
+    for args in ((-1, 8, 8, 8), (1, 0, 8, 8), (1, 8, 8, 257), ((1 << 30) + 1, 8, 8, 8)):
         with pytest.raises(Q.QloraError) as e:
             Q.qlora_f8_linear_workspace(*args)
         assert e.value.status == Q.QLORA_ERR_SHAPE

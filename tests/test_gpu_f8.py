@@ -119,3 +119,81 @@ def test_matmul(m, n, k, trans):
         Q.qlora_f8_matmul(a, b, trans, out=out)
         _check_product(a, b, trans, out)
         assert (guard[:128] == 7).all() and (guard[128 + m * n:] == 7).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(7, 300, 520), (70, 300, 520), (2500, 2304, 400)])
+@pytest.mark.parametrize("trans", [True, False])
+def test_bad_values_stay_in_their_row_and_column(m, n, k, trans):
+    """NaN and infinities of A spoil their rows of C, those of B their columns, nothing else."""
+    x = _x(m, k, 1, torch.float32)
+    w = _x(n, k, 2, torch.float32)
+    clean = Q.qlora_f8_matmul(
+        Q.qlora_f8_quantize(x.to(DEV)),
+        Q.qlora_f8_quantize((w if trans else w.t().contiguous()).to(DEV), Q.QLORA_F8_TILES), trans)
+    x[3, 5], x[m - 1, k - 1] = float("nan"), float("inf")
+    w[4, 130], w[n - 1, 0] = -float("inf"), float("nan")
+    a = Q.qlora_f8_quantize(x.to(DEV))
+    b = Q.qlora_f8_quantize((w if trans else w.t().contiguous()).to(DEV), Q.QLORA_F8_TILES)
+    got = Q.qlora_f8_matmul(a, b, trans).float().cpu().numpy()
+    bad = np.zeros((m, n), bool)
+    bad[[3, m - 1]] = True
+    bad[:, [4, n - 1]] = True
+    assert np.isnan(got[bad]).all() and np.isfinite(got[~bad]).all()
+    # a spoilt value leaves the scale of its block to the others: the rest may move where it
+    # was the block's largest, by a rounding of the codes (2^-4 of a value) at most
+    rest = clean.float().cpu().numpy()
+    scale = np.abs(R.restore(np.nan_to_num(a.values.float().cpu().numpy()), a.scales.cpu().numpy(),
+                             "rows", np.float64)) @ np.abs(np.nan_to_num(w.numpy().T, posinf=0, neginf=0))
+    assert (np.abs(got - rest)[~bad] <= 0.3 * scale[~bad] + 1e-30).all()
+
+
+@pytest.mark.parametrize("m,n,k,trans", [(1, 1000, 300, True), (40, 500, 300, False),
+                                         (2500, 2304, 400, True), (2500, 2304, 400, False)])
+def test_padding_is_not_read(m, n, k, trans):
+    """Rows of codes padded with NaN bytes, a larger ld than needed: the same product."""
+    a, b = _matrices(m, n, k, trans, "e4m3", "e4m3", False, 5)
+    want = Q.qlora_f8_matmul(a, b, trans)
+
+    def padded(q):
+        codes = torch.full((q.rows, q.codes.shape[1] + 32), 0x7f, dtype=torch.uint8, device=DEV)
+        codes[:, :q.cols] = q.codes[:, :q.cols]
+        return Q.F8Matrix(q.rows, q.cols, q.layout, q.format, q.pow2, codes, q.scales)
+    assert torch.equal(Q.qlora_f8_matmul(padded(a), padded(b), trans), want)
+    assert torch.equal(Q.qlora_f8_dequantize(padded(a)), Q.qlora_f8_dequantize(a))
+
+
+def test_two_streams_at_once():
+    """Calls without a workspace share nothing: two streams, interleaved, give what one gives."""
+    sets = [_matrices(m, 1024, 2048, True, "e4m3", "e4m3", False, m) for m in (4, 100, 1500, 3000)]
+    want = [Q.qlora_f8_matmul(a, b) for a, b in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for i in range(4):
+        for j, (a, b) in enumerate(sets):
+            s = streams[(i + j) % 2]
+            got.append((j, Q.qlora_f8_matmul(a, b, stream=s), Q.qlora_f8_dequantize(a, stream=s)))
+    torch.cuda.synchronize()
+    for j, c, x in got:
+        assert torch.equal(c, want[j])
+        assert torch.equal(x, Q.qlora_f8_dequantize(sets[j][0]))
+
+
+def test_deterministic_and_out():
+    a, b = _matrices(33, 640, 4096, True, "e4m3", "e4m3", False, 3)
+    c = Q.qlora_f8_matmul(a, b, dtype=torch.float32)
+    out = torch.empty_like(c)
+    assert Q.qlora_f8_matmul(a, b, out=out) is out and torch.equal(out, c)
+    with pytest.raises(ValueError):
+        Q.qlora_f8_matmul(a, b, out=torch.empty(640, 33, device=DEV))
+    with pytest.raises(ValueError):
+        Q.qlora_f8_matmul(a, b, out=torch.empty(33, 640, dtype=torch.float16, device=DEV))
+    with pytest.raises(Q.QloraError):
+        Q.qlora_f8_matmul(b, a.__class__.empty(33, 4096, Q.QLORA_F8_TILES))  # b is not by rows
+    x = torch.zeros(4, 64, device=DEV)
+    with pytest.raises(ValueError):
+        Q.qlora_f8_quantize(x, out=Q.F8Matrix.empty(5, 64))
+    with pytest.raises(ValueError):
+        Q.qlora_f8_quantize(x[:, ::2])
+    with pytest.raises(ValueError):
+        Q.qlora_f8_quantize(x.half())

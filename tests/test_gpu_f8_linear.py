@@ -265,3 +265,59 @@ def test_on_another_stream():
     s.synchronize()
     for a, b in zip(want, got):
         assert torch.equal(a, b)
+
+
+def test_gradients_against_differences():
+    """dX, dA, dB of the layer over the 8-bit base against central differences of its loss in
+    fp64, from the operands as they are held in 8 bits (the layer's own definition)."""
+    M, N, K, r, s = 6, 16, 24, 8, 2.0
+    W, A, B, X, dY = _rand_case(M, N, K, r, 11)
+    w8 = Q.qlora_f8_quantize(W.to(DEV), Q.QLORA_F8_TILES, pow2=True)
+    U = torch.empty((M, r), dtype=torch.float32, device=DEV)
+    x8 = Q.F8Matrix.empty(M, K, pow2=True)
+    Q.qlora_f8_linear_fwd(w8, A.to(DEV), B.to(DEV), s * r, X.to(DEV), x8, U_save=U)
+    dX, dA, dB = Q.qlora_f8_linear_bwd(w8, A.to(DEV), B.to(DEV), s * r, x8, U, dY.to(DEV),
+                                       Q.QLORA_E4M3, check=True)
+    xq = R.restore(*R.quantize(X, "rows", "e4m3", True), "rows", np.float64)
+    wq = R.restore(*R.quantize(W, "tiles", "e4m3", True), "tiles", np.float64)
+    dq = R.restore(*R.quantize(dY, "rows", "e4m3", True), "rows", np.float64)
+    a, b, dy = _f(A), _f(B), _f(dY)
+
+    def diff(f, v):
+        g = np.zeros_like(v)
+        for i in np.ndindex(v.shape):
+            h = 1e-4
+            v[i] += h
+            up = f()
+            v[i] -= 2 * h
+            g[i] = (up - f()) / (2 * h)
+            v[i] += h
+        return g
+    # the loss is linear in each argument: differences are exact to rounding
+    da = diff(lambda: float((dy * (s * (xq @ a.T) @ b.T)).sum()), a)
+    db = diff(lambda: float((dy * (s * (_f(X) @ a.T) @ b.T)).sum()), b)
+    x = xq.copy()
+    dx = diff(lambda: float((dq * (x @ wq.T)).sum() + (dy * (s * (x @ a.T) @ b.T)).sum()), x)
+    for got, want, tol in ((dA, da, 2.0 ** -14), (dB, db, 2.0 ** -14), (dX, dx, 2.0 ** -7)):
+        assert np.abs(_f(got) - want).max() <= tol * np.abs(want).max()
+
+
+def test_timed_and_counted():
+    """With kernel timing on (event records between the launches) the results are the same."""
+    M, N, K, r = 200, 256, 512, 16
+    W, A, B, X, dY = (t.to(DEV) for t in _rand_case(M, N, K, r, 12))
+    w8 = Q.qlora_f8_quantize(W, Q.QLORA_F8_TILES)
+    U = torch.empty((M, r), dtype=torch.float32, device=DEV)
+
+    def step():
+        x8 = Q.F8Matrix.empty(M, K)
+        y = Q.qlora_f8_linear_fwd(w8, A, B, 16.0, X, x8, U_save=U, check=True)
+        return [y, *Q.qlora_f8_linear_bwd(w8, A, B, 16.0, x8, U, dY, check=True)]
+    want, n0 = step(), Q.qlora_launch_count()
+    Q.qlora_timing_begin([Q.QLORA_KERNEL_QUANTIZE, Q.QLORA_KERNEL_LORA_GEMM])
+    got = step()
+    t = Q.qlora_timing_end()
+    assert Q.qlora_launch_count() - n0 >= 8
+    assert t[Q.QLORA_KERNEL_QUANTIZE][1] == 2 and t[Q.QLORA_KERNEL_LORA_GEMM][1] >= 3
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
