@@ -56,7 +56,7 @@ struct Cfg {
   static constexpr int kPerSm = SWAP ? 2 : 1;
   static constexpr int kThreads = 128 + 32 * kEpi;  // TMA, MMA, scales, one idle; the sums
   static constexpr int kCols = BN / (kEpi / 4);   // accumulator columns per thread
-  static constexpr int kBufs = BN >= 128 ? 2 : 4; // TMEM accumulators in flight
+  static constexpr int kBufs = 4; // TMEM accumulators in flight
   static constexpr int kTmem = BN * kBufs;        // 64, 128 or 256 columns
   using Ring = f8::ScaleRing<SWAP ? BN : 128, 1>;
   static constexpr int kQBytes = BN * 128;
