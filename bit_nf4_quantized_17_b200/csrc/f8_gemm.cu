@@ -23,8 +23,12 @@
 // shared memory in split order (deterministic).
 //
 // Roles: warp 0 TMA producer, warp 1 TMEM owner and MMA issuer, warp 2 the
-// scales, the 4 or 8 warps from warp 4 on drain the accumulators.  Every wait is bounded; the call has no
-// status word, so a CTA whose wait gives up writes NaN to its part.
+// scales, the 4 or 8 warps from warp 4 on drain the accumulators.  Every wait is
+// bounded; the call has no status word, so a CTA whose wait gives up writes NaN to its
+// part.
+//
+// Bound by the bytes of B for few tokens (1 x 11008 x 4096 in 11 us from HBM, 45 MB), by
+// its fixed costs (launch, first loads, cluster sum: 6 us) up to a few hundred.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -56,7 +60,9 @@ struct Cfg {
   static constexpr int kPerSm = SWAP ? 2 : 1;
   static constexpr int kThreads = 128 + 32 * kEpi;  // TMA, MMA, scales, one idle; the sums
   static constexpr int kCols = BN / (kEpi / 4);   // accumulator columns per thread
-  static constexpr int kBufs = 4; // TMEM accumulators in flight
+  // TMEM accumulators in flight (two of 128 columns: 22 us instead of 18.8 for
+  // 256 x 11008 x 4096)
+  static constexpr int kBufs = 4;
   static constexpr int kTmem = BN * kBufs;        // 64, 128 or 256 columns
   using Ring = f8::ScaleRing<SWAP ? BN : 128, 1>;
   static constexpr int kQBytes = BN * 128;

@@ -2,24 +2,34 @@
 // CTA pairs: the large form of f8_gemm.cu (same product, same LoRA term).
 //
 // A cluster of two CTAs computes 256 x 256 tiles of C with pair MMAs
-// (tcgen05.mma.cta_group::2, M = 256, N = 256, issued by the even CTA): each
-// CTA holds its 128 rows of A and half of the B tile, and its TMEM receives its
-// 128 x 256 sums.  A 128-deep block is 512 cycles of MMA; it goes into one of two
-// TMEM accumulators (all 512 columns), and eight warps add the finished one,
-// times its scales, to 128 fp32 sums per thread: 128 multiply-adds and TMEM words
-// per thread and block, about half the MMA's time, so the tensor cores stay fed.
-// A warp's 128 columns lie in one scale block of B, so a thread needs one scale
-// per block.
+// (tcgen05.mma.cta_group::2, M = 256, issued by the even CTA): each CTA holds its 128
+// rows of A and half of the B tile, and its TMEM receives its 128 rows' sums.  A
+// 128-deep block is two products of N = 128 (64 columns of either CTA's half each),
+// 256 cycles apiece, into one of two TMEM accumulators of their own (four in all:
+// the 512 columns).  Four warps drain each half: 128 fp32 sums a thread, times the
+// block's scales, in packed multiply-adds (two a register pair: no faster per
+// sum than scalar ones, but they leave every other issue slot to the MMA issuer,
+// which shares an SM quarter with two of these warps: 326 against 338 us below).
+// Halves rather than one N = 256 product per block keep the MMAs and the sums of
+// either group out of step with each other (one product: 340 us), and the tensor
+// cores work on two accumulators while two are drained.  With one thread a row and
+// 128 columns a thread needs one scale of A and two of B per block.
+//
+// Bound: 2048 x 8192 x 22016 takes 326 us in bursts (2.27 PFLOP/s), the same MMAs
+// without sums 250 us; sustained, the 1 kW power cap lowers the clock to 1.48 GHz
+// and it takes 390-400 us.  4096^3: 72 us.
 //
 // The kernel is persistent: a pair takes tiles pair, pair + pairs, ..., and
-// while its epilogue warps store a tile the next tile's first two blocks run.
-// Tiles go down 16 row tiles before the next column tile, so that the pairs at
-// work share a few columns of B and rows of A that stay in L2.
+// while its sum warps store a tile the next tile's first blocks run.  Tiles go
+// down 16 row tiles before the next column tile, so that the pairs at work share a few
+// columns of B and rows of A that stay in L2.
 //
 // Roles per CTA (384 threads): warp 0 TMA producer, warp 1 TMEM and, in the
-// even CTA, the MMA issuer, warp 2 the scales, warps 4-11 the sums.  TMA loads of both CTAs count on the
-// even CTA's barriers (no multicast).  Every wait is bounded; a CTA whose wait
-// gives up writes NaN to what it had not finished.
+// even CTA, the MMA issuer, warp 2 the scales, warps 4-11 the sums.  The sums and the
+// words on their way are 192 registers a thread: the role warps hand theirs over
+// (40 against 232).  TMA loads of both CTAs count on the even CTA's barriers (no
+// multicast).  Every wait is bounded; a CTA whose wait gives up writes NaN to what it
+// had not finished.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -37,6 +47,7 @@ using f8::store_run;
 constexpr int kEpi = 8;
 constexpr int kRoleWarps = 4;                // TMA, MMA, scales, one idle
 constexpr int kThreads = 32 * (kRoleWarps + kEpi);
+constexpr int kRoleRegs = 40, kSumRegs = 232;  // registers a thread, from 168 at launch
 constexpr int kStages = 5;
 constexpr int kOpBytes = 16384;              // 128 rows x 128 bytes: A, and this CTA's half of B
 constexpr int kStageBytes = 2 * kOpBytes;
@@ -111,7 +122,7 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   // (The loops of the two issuing threads step the stage, its phase and the
   // descriptors with adds only: see f8_gemm.cu.)
   if (warp < kRoleWarps) {
-  ptx::setmaxnreg_dec<40>();
+  ptx::setmaxnreg_dec<kRoleRegs>();
   if (warp == 0 && ptx::elect_one()) {
     // ------------------------------------------------------ TMA producer
     // the launch may start before the one ahead of it is done: everything before
@@ -274,7 +285,7 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   }
   } else {
     // ------------------------------------------------------ sums
-    ptx::setmaxnreg_inc<232>();
+    ptx::setmaxnreg_inc<kSumRegs>();
     // warps 4-7 add the accumulators of the first half of each block, warps 8-11
     // those of the second: columns [64 h, 64 h + 64) and [128 + 64 h, ...) of the tile
     const int quarter = warp & 3, h = (warp - kRoleWarps) >> 2;
@@ -450,8 +461,24 @@ qlora_status f8_gemm_pairs(const qlora_f8& a, const qlora_f8& b, bool trans_b, v
   p.n_tiles = static_cast<int32_t>(ceil_div(n, 256));
   const int64_t tiles = ceil_div(m, 256) * p.n_tiles;
   if (tiles > 0x3fffffff) return QLORA_ERR_SHAPE;
-  const qlora_status cs = ensure_smem(reinterpret_cast<const void*>(f8_pair_kernel), kSmemBytes);
+  const void* fn = reinterpret_cast<const void*>(f8_pair_kernel);
+  const qlora_status cs = ensure_smem(fn, kSmemBytes);
   if (cs != QLORA_OK) return cs;
+  // the sum warps' larger share comes out of the registers of the launch: a build that
+  // launches with fewer would wait for them forever
+  constexpr int kRegsTag = 1;
+  int regs = 0;
+  if (!cached_value(fn, kRegsTag, &regs)) {
+    cudaFuncAttributes attr;
+    if (cudaFuncGetAttributes(&attr, f8_pair_kernel) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return QLORA_ERR_CUDA;
+    }
+    regs = attr.numRegs;
+    store_value(fn, kRegsTag, regs);
+  }
+  if (regs * kThreads < 32 * (kRoleWarps * kRoleRegs + kEpi * kSumRegs))
+    return QLORA_ERR_UNSUPPORTED;
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess)
     (void)cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
