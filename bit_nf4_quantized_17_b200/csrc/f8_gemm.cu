@@ -544,14 +544,21 @@ qlora_status f8_gemm(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c
   const int64_t m = p.m, n = p.n;
   if (m <= 16) return launch<16, true>(a, b, trans_b, p, l, s);
   if (m <= 32) return launch<32, true>(a, b, trans_b, p, l, s);
-  // single CTAs or pairs, whichever ends sooner: a pair's 256 x 256 block takes 1.5
-  // times a CTA's 128 x 128 block (0.47 against 0.32 us).  At k = 4096: 384 x 11008
-  // in 28 us on CTAs, 42 us on pairs; 4096 x 4096 in 112 and 76 us.
+  // whichever ends soonest: rounds of tiles times what a 128-deep block of a tile takes
+  // (0.32 us for 128 x 128 on a CTA, 0.46 for 256 x 256 on a pair, 0.28 for 256 x 192 on a
+  // pair with power-of-two scales).  At k = 4096: 384 x 11008 in 26 us on CTAs, 42 on
+  // pairs; 4096 x 4096 in 112, 70 and 52 us; 1024 x 4096 in 21 on pairs, 22.5 as powers.
   const int sms = f8::sm_count();
-  const int64_t tiles = ceil_div(n, 128) * ceil_div(m, 128);
-  const int64_t one = ceil_div(tiles, sms);
-  const int64_t two = ceil_div(ceil_div(n, 256) * ceil_div(m, 256), sms / 2);
-  if (tiles > sms && 2 * one > 3 * two) return f8_gemm_pairs(a, b, trans_b, c, c_f32, l, s);
+  const int64_t tiles = ceil_div(n, 128) * ceil_div(m, 128), m2 = ceil_div(m, 256);
+  if (tiles > sms) {
+    const int64_t pairs = sms / 2;
+    const int64_t one = 32 * ceil_div(tiles, sms);
+    const int64_t two = 46 * ceil_div(m2 * ceil_div(n, 256), pairs);
+    const int64_t pow2 = 28 * ceil_div(m2 * ceil_div(n, 192), pairs);
+    if (a.pow2 && b.pow2 && pow2 < std::min(one, two))
+      return f8_gemm_pow2(a, b, trans_b, c, c_f32, l, s);
+    if (two < one) return f8_gemm_pairs(a, b, trans_b, c, c_f32, l, s);
+  }
   return launch<128, false>(a, b, trans_b, p, l, s);
 }
 

@@ -141,5 +141,8 @@ GemmArgs gemm_args(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, 
 // f8_gemm2.cu: the product on CTA pairs, for sizes whose 256 x 256 tiles fill the GPU.
 qlora_status f8_gemm_pairs(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,
                            const F8Lora& lora, cudaStream_t s);
+// f8_gemm_pow2.cu: the same where every scale of a and b is a power of two.
+qlora_status f8_gemm_pow2(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,
+                          const F8Lora& lora, cudaStream_t s);
 
 }  // namespace qlora

@@ -303,7 +303,8 @@ qlora_status qlora_linear_bwd_ex(const qlora_nf4* W, const void* A, const void* 
  *           QLORA_F8_TILES: a scale per 128 x 128 tile, row-major:
  *           scales[(row / 128) * ceil(cols / 128) + col / 128] (weights)
  *   format  QLORA_E4M3 (largest value F = 448) or QLORA_E5M2 (F = 57344)
- *   pow2    1: the scales are powers of two, 0: any fp32
+ *   pow2    1: every scale is a power of two (a product may then read its exponent
+ *           only), 0: any fp32
  *   codes   device, rows of ld bytes (ld a multiple of 16, at least cols)
  *   scales  device fp32
  * The value of an element is its code times its block's scale.  Sizes need not

@@ -179,6 +179,30 @@ def test_two_streams_at_once():
         assert torch.equal(x, Q.qlora_f8_dequantize(sets[j][0]))
 
 
+@pytest.mark.parametrize("m,n,k,trans", [(2500, 2568, 1111, True), (2500, 2568, 1111, False),
+                                         (4300, 4105, 130, True), (2304, 4096, 2048, False)])
+@pytest.mark.parametrize("fa,fb", [("e4m3", "e4m3"), ("e5m2", "e4m3"), ("e4m3", "e5m2")])
+def test_power_of_two_scales_on_the_tensor_core(m, n, k, trans, fa, fb):
+    """The same matrices told to be powers of two or not: the same sums, up to their order.
+    Scales from 2^-126 (rows of zeros) to large ones, blocks past a group of four."""
+    x, w = _x(m, k, 21, torch.float32), _x(n, k, 22, torch.float32)
+    x[5] = 0
+    x[6, :128] *= 2.0 ** 60
+    x[7] *= 2.0 ** -100
+    w = w if trans else w.t().contiguous()
+    a = Q.qlora_f8_quantize(x.to(DEV), Q.QLORA_F8_ROWS, FORMAT[fa], True)
+    b = Q.qlora_f8_quantize(w.to(DEV), Q.QLORA_F8_TILES, FORMAT[fb], True)
+    told = Q.qlora_f8_matmul(a, b, trans, torch.float32)
+    as_any = [Q.F8Matrix(q.rows, q.cols, q.layout, q.format, False, q.codes, q.scales)
+              for q in (a, b)]
+    untold = Q.qlora_f8_matmul(*as_any, trans, torch.float32)
+    _check_product(a, b, trans, told)
+    _check_product(a, b, trans, untold)
+    assert (told[5] == 0).all() and (untold[5] == 0).all()
+    mixed = Q.qlora_f8_matmul(a, as_any[1], trans, torch.float32)  # one of the two is told
+    assert torch.equal(mixed, untold)
+
+
 def test_deterministic_and_out():
     a, b = _matrices(33, 640, 4096, True, "e4m3", "e4m3", False, 3)
     c = Q.qlora_f8_matmul(a, b, dtype=torch.float32)
