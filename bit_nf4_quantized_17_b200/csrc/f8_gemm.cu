@@ -107,6 +107,7 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
   const bool p_mn = SWAP && p.b_mn, q_mn = !SWAP && p.b_mn;
   const bool p2_mn = SWAP && p.ext_mn, q2_mn = !SWAP && p.ext_mn;
 
+  ptx::grid_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       ptx::mbar_init(&full[s], 1);

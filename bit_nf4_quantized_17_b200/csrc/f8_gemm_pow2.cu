@@ -86,6 +86,7 @@ f8_pow2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int tiles = m_tiles * p.n_tiles;
   const int kn = p.kb_total;
 
+  ptx::grid_launch_dependents();
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&full[s], 1);

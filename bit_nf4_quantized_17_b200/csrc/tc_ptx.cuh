@@ -147,6 +147,12 @@ __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// Let a dependent launch that follows start once every CTA of this one has: it still
+// waits (grid_dependency_wait) for this one's end before it reads or writes.
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------- registers
 // Hand registers from the warps of one warpgroup to those of another (all four
 // warps of a warpgroup execute it; the shares add up to what the launch has).
