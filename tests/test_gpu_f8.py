@@ -221,3 +221,34 @@ def test_deterministic_and_out():
         Q.qlora_f8_quantize(x[:, ::2])
     with pytest.raises(ValueError):
         Q.qlora_f8_quantize(x.half())
+
+
+def test_past_32_bits():
+    """More than 2^31 elements: quantise, restore and both products, checked on the last rows
+    and columns against the same rows and columns alone."""
+    m, n, k = 66000, 33008, 256
+    g = torch.Generator(DEV).manual_seed(1)
+    big = torch.randn(m, n, generator=g, device=DEV, dtype=torch.bfloat16)
+    q = Q.qlora_f8_quantize(big, pow2=True)
+    tail = Q.qlora_f8_quantize(big[-300:].contiguous(), pow2=True)
+    assert torch.equal(q.codes[-300:], tail.codes)
+    assert torch.equal(q.scales[:, -300:], tail.scales)
+    assert torch.equal(Q.qlora_f8_dequantize(q)[-300:], Q.qlora_f8_dequantize(tail))
+    t = Q.qlora_f8_quantize(big[:128 * 515], Q.QLORA_F8_TILES)
+    tt = Q.qlora_f8_quantize(big[128 * 512:128 * 515].contiguous(), Q.QLORA_F8_TILES)
+    assert torch.equal(t.codes[128 * 512:], tt.codes) and torch.equal(t.scales[512:], tt.scales)
+    del big, t
+    a = Q.qlora_f8_quantize(torch.randn(m, k, generator=g, device=DEV))
+    b = Q.qlora_f8_quantize(torch.randn(n, k, generator=g, device=DEV), Q.QLORA_F8_TILES)
+    c = Q.qlora_f8_matmul(a, b)  # 2.2e9 outputs
+
+    def rows(x, at):
+        return Q.F8Matrix(x.rows - at, x.cols, x.layout, x.format, x.pow2, x.codes[at:].contiguous(),
+                          x.scales[:, at:].contiguous())
+    assert torch.equal(c[65536:], Q.qlora_f8_matmul(rows(a, 65536), b))
+    del c
+    # a left operand of more than 2^31 codes against few columns, both directions' contraction
+    w = Q.qlora_f8_quantize(torch.randn(64, n, generator=g, device=DEV), Q.QLORA_F8_TILES)
+    y = Q.qlora_f8_matmul(q, w, dtype=torch.float32)
+    want = Q.qlora_f8_matmul(rows(q, 65792), w, dtype=torch.float32)
+    assert float((y[65792:] - want).abs().max()) <= 1e-5 * float(want.abs().max())
