@@ -15,9 +15,9 @@
 // cores work on two accumulators while two are drained.  With one thread a row and
 // 128 columns a thread needs one scale of A and two of B per block.
 //
-// Bound: 2048 x 8192 x 22016 takes 326 us in bursts (2.27 PFLOP/s), the same MMAs
+// Bound: 2048 x 8192 x 22016 takes 322 us in bursts (2.3 PFLOP/s), the same MMAs
 // without sums 250 us; sustained, the 1 kW power cap lowers the clock to 1.48 GHz
-// and it takes 390-400 us.  4096^3: 72 us.
+// and it takes 384 us.  4096^3: 70 us.
 //
 // The kernel is persistent: a pair takes tiles pair, pair + pairs, ..., and
 // while its sum warps store a tile the next tile's first blocks run.  Tiles go

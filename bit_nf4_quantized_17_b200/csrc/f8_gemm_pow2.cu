@@ -15,6 +15,9 @@
 // Four warps, one a quarter, build the words from the fp32 scales (exponent bits) and store
 // them with tcgen05.st, up to four groups ahead.
 //
+// Bound: 2048 x 8192 x 8192 in 100 us in bursts (2.75 PFLOP/s, fp32 scales 125 us), 119 us
+// sustained under the 1 kW power cap; 4096^3 in 52 us.
+//
 // A pair computes 256 x 192 tiles: two accumulators of 192 columns (one is drained
 // while the next tile is summed) and the exponents fit the 512 TMEM columns, and
 // 192 divides better into rounds than 256: 2048 x 8192 is 3.75 rounds' work instead
