@@ -449,6 +449,21 @@ int split_count(int64_t tiles, int64_t kb, int64_t slots) {
   return static_cast<int>(std::max<int64_t>(1, s));
 }
 
+// Clusters of `splits` CTAs that run at once, asked for once per kernel, size and
+// device.  (For the kernel of one CTA per SM: a split has at least 4 blocks, so 4 stages,
+// 128 KB, and the answer does not depend on how many more it has.)
+int resident_clusters(const void* fn, const cudaLaunchConfig_t& cfg, int splits) {
+  constexpr int kClusterTag = 16;
+  int n = 0;
+  if (cached_value(fn, kClusterTag + splits, &n)) return n;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    n = 0;
+  }
+  store_value(fn, kClusterTag + splits, n);
+  return n;
+}
+
 template <int BN, bool SWAP>
 qlora_status launch(const qlora_f8& a, const qlora_f8& b, bool trans_b, GemmArgs p,
                     const F8Lora& l, cudaStream_t s) {
@@ -477,32 +492,39 @@ qlora_status launch(const qlora_f8& a, const qlora_f8& b, bool trans_b, GemmArgs
   const int64_t p_tiles = ceil_div(SWAP ? n : m, 128), q_tiles = ceil_div(SWAP ? m : n, BN);
   p.n_tiles = static_cast<int32_t>(q_tiles);
   if (p_tiles * q_tiles > 0x7fffffff) return QLORA_ERR_SHAPE;
-  const int sms = f8::sm_count();
-  const int splits = split_count(p_tiles * q_tiles, p.kb_total, C::kPerSm * sms);
-  p.kb_per = static_cast<int32_t>(ceil_div(p.kb_total, splits));
-  // the stages that fit beside as many CTAs as an SM gets; no more than a split has blocks
-  const int64_t want = p.kb_per + p.ext_tiles;
-  const bool two = C::kPerSm == 2 && p_tiles * q_tiles * splits > sms;
-  p.stages = static_cast<int32_t>(
-      std::min<int64_t>({kMaxStages, want, ((two ? 100 : 200) * 1024) / C::kStage}));
   const void* fn = reinterpret_cast<const void*>(f8_gemm_kernel<BN, SWAP>);
   const qlora_status cs = ensure_smem(fn, 220 * 1024);
   if (cs != QLORA_OK) return cs;
+  const int sms = f8::sm_count();
+  const int64_t tiles = p_tiles * q_tiles;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p_tiles * q_tiles), 1, static_cast<unsigned>(splits));
   cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes =
-      1024 + std::max(p.stages * C::kStage, C::kRedBytes) + sizeof(typename C::Ring) + 512;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1;
   attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
-  cfg.attrs = attr;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
   cfg.numAttrs = 2;
+  for (int splits = split_count(tiles, p.kb_total, C::kPerSm * sms);; --splits) {
+    p.kb_per = static_cast<int32_t>(ceil_div(p.kb_total, splits));
+    // the stages that fit beside as many CTAs as an SM gets; no more than a split has blocks
+    const int64_t want = p.kb_per + p.ext_tiles;
+    const bool two = C::kPerSm == 2 && tiles * splits > sms;
+    p.stages = static_cast<int32_t>(
+        std::min<int64_t>({kMaxStages, want, ((two ? 100 : 200) * 1024) / C::kStage}));
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles), 1, static_cast<unsigned>(splits));
+    cfg.dynamicSmemBytes =
+        1024 + std::max(p.stages * C::kStage, C::kRedBytes) + sizeof(typename C::Ring) + 512;
+    attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
+    // A cluster lies within one group of SMs, so of size 8 at one CTA per SM fewer than 16
+    // run at once: 256 x 1024 x 4096, 16 tiles, took 14.2 us in 8 splits and takes 7.9 in
+    // as many as do.  Two CTAs per SM read for one another while some wait: 16 x 11008 x
+    // 4096, 86 tiles, 7.8 us in 3 splits, 10.3 in the 2 that would all be resident.
+    if (C::kPerSm == 2 || splits == 1 || tiles <= resident_clusters(fn, cfg, splits)) break;
+  }
   count_launch();
   const cudaError_t e = cudaLaunchKernelEx(&cfg, f8_gemm_kernel<BN, SWAP>, SWAP ? mb : ma,
                                            SWAP ? ma : mb, SWAP ? mr : ml, SWAP ? ml : mr, p);
