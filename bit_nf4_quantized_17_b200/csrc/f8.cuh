@@ -30,6 +30,9 @@ struct F8Lora {
   const void* L;
   const void* R;
   int32_t r;  // 0 = no LoRA term
+  // The launches ahead of the product belong to the same call and write neither B nor R,
+  // and the first of them began when everything before it was done: B may be read at once.
+  bool b_ready = false;
 };
 
 // f8_gemm.cu: C (m x n, row-major, bf16 or fp32) = A . B^T (trans_b) or A . B,

@@ -149,8 +149,29 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
   // in them cost 600 and 1100 cycles a block, more than the block's bytes or MMAs.)
   if (warp == 0 && ptx::elect_one()) {
     // ------------------------------------------------------ TMA producer
-    // the launch may start before the one ahead of it is done: everything before
-    // this touched no memory of the caller's, everything after follows these loads
+    auto load_p = [&](int st, uint8_t* dst, int k) {
+      if (p_mn)
+        ptx::tma_load_2d(&tmP, &full[st], dst, p0, k);
+      else
+        ptx::tma_load_2d(&tmP, &full[st], dst, k, p0);
+    };
+    auto load_q = [&](int st, uint8_t* dst, int k) {
+      if (q_mn)
+        ptx::tma_load_2d(&tmQ, &full[st], dst + kPBytes, q0, k);
+      else
+        ptx::tma_load_2d(&tmQ, &full[st], dst + kPBytes, k, q0);
+    };
+    // The launch may start before those ahead of it are done.  Until they are it reads
+    // nothing but a B that they do not write: as many of its tiles as there are stages
+    // (decoding: often all), so that the weight streams in under their latency.
+    const int early = p.b_ready ? min(kn, p.stages) : 0;
+    for (int i = 0, k = kb0 * 128; i < early; ++i, k += 128) {
+      ptx::mbar_arrive_expect_tx(&full[i], C::kStage);
+      if (SWAP)
+        load_p(i, smem + i * C::kStage, k);
+      else
+        load_q(i, smem + i * C::kStage, k);
+    }
     ptx::grid_dependency_wait();
     int s = 0, issued = 0;
     uint32_t ph = 1;
@@ -166,17 +187,13 @@ f8_gemm_kernel(const __grid_constant__ CUtensorMap tmP, const __grid_constant__ 
       }
     };
     for (int i = 0, k = kb0 * 128; i < kn; ++i, k += 128) {
-      go = ptx::mbar_wait(&empty[s], ph, kTimeoutCycles, abort_flag);
-      if (!go) break;
-      ptx::mbar_arrive_expect_tx(&full[s], C::kStage);
-      if (p_mn)
-        ptx::tma_load_2d(&tmP, &full[s], sp, p0, k);
-      else
-        ptx::tma_load_2d(&tmP, &full[s], sp, k, p0);
-      if (q_mn)
-        ptx::tma_load_2d(&tmQ, &full[s], sp + kPBytes, q0, k);
-      else
-        ptx::tma_load_2d(&tmQ, &full[s], sp + kPBytes, k, q0);
+      if (i >= early) {
+        go = ptx::mbar_wait(&empty[s], ph, kTimeoutCycles, abort_flag);
+        if (!go) break;
+        ptx::mbar_arrive_expect_tx(&full[s], C::kStage);
+      }
+      if (!SWAP || i >= early) load_p(s, sp, k);
+      if (SWAP || i >= early) load_q(s, sp, k);
       next();
     }
     for (int t = 0, h = 0; t < ext && go; ++t) {
@@ -552,6 +569,7 @@ f8::GemmArgs f8::gemm_args(const qlora_f8& a, const qlora_f8& b, bool trans_b, v
   p.c = c;
   p.c_ld = p.n;
   p.c_f32 = c_f32 ? 1 : 0;
+  p.b_ready = l.b_ready ? 1 : 0;
   if (l.r > 0) {
     p.ext_half = (l.r + 63) / 64;
     p.ext_tiles = 2 * p.ext_half;

@@ -18,6 +18,7 @@ struct GemmArgs {
   int32_t b_mn;                // B MN-major: its contraction axis is its rows
   int32_t ext_tiles, ext_half, ext_last_steps, ext_mn;
   int32_t c_f32;
+  int32_t b_ready;             // B may be read before the launches ahead are done
   int32_t c_tma;               // C leaves through TMA stores (CTA pairs)
   const float* sa;             // A's scales, [kb][m]
   const float* sb;             // B's scales: block column nb at sb[nb * sb_n + kb * sb_k]

@@ -82,9 +82,10 @@ qlora_status f8_linear_forward(const qlora_f8& W, const void* A, const void* B, 
     ra.o2_pad = 1;
     QLORA_TRY(tc_rank_gemm(X, false, M, K, K, A, false, K, r, r16, ra, st, s));
   }
-  // beside the U launch, which starts when all work before it is done and shares only X
+  // beside the U launch, which starts when all work before it is done and shares only X;
+  // the product starts beside both and reads W at once (8 x 4096 x 4096: 13.5 -> 11.3 us)
   QLORA_TRY(launch_f8_quantize(X, QLORA_BF16, x8, s, true));
-  return f8_gemm(x8, W, true, Y, false, F8Lora{su, B, r}, s);
+  return f8_gemm(x8, W, true, Y, false, F8Lora{su, B, r, true}, s);
 }
 
 qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B, int32_t r,
@@ -134,7 +135,7 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
     return QLORA_ERR_CUDA;
   auto main_work = [&]() -> qlora_status {
     if (!dX) return QLORA_OK;
-    return f8_gemm(dy8, W, false, dX, false, F8Lora{sv, A, r}, s);
+    return f8_gemm(dy8, W, false, dX, false, F8Lora{sv, A, r, true}, s);
   };
   auto side_work = [&]() -> qlora_status {
     if (small) {

@@ -175,6 +175,9 @@ __device__ __forceinline__ void end_beside_last() {
 // consecutive rows are one store.
 template <typename T, bool E5M2, bool VEC, int ROWS>
 __global__ void __launch_bounds__(kThreads) f8_rows_kernel(const QArgs p) {
+  // the product that follows may start: it waits for the end of this launch before it
+  // reads what this one writes
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kPer = ROWS / 8;  // rows per warp
   __shared__ float sc[4][ROWS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
