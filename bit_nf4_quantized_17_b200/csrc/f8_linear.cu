@@ -67,9 +67,7 @@ qlora_status f8_linear_forward(const qlora_f8& W, const void* A, const void* B, 
   char* su = ws + L.su;
   // U = X A^T -> U_save (fp32) and sU = s U as bf16 hi + lo
   if (M <= kSmallM) {
-    const RankOut ro{r, U_save, r, 1.0f, reinterpret_cast<__nv_bfloat16*>(su), 2 * span,
-                     sc, span, nullptr, r};
-    QLORA_TRY(rank_down(X, A, static_cast<int>(M), K, span, ro, s));
+    QLORA_TRY(f8_front(X, x8, A, r, sc, U_save, su, s));  // and the 8 bits of X
   } else {
     ReduceArgs ra = reduce_args(nullptr, 1, M, r, r16);
     ra.o1 = U_save;
@@ -81,10 +79,10 @@ qlora_status f8_linear_forward(const qlora_f8& W, const void* A, const void* B, 
     ra.o2_lo = span;
     ra.o2_pad = 1;
     QLORA_TRY(tc_rank_gemm(X, false, M, K, K, A, false, K, r, r16, ra, st, s));
+    // beside the U launch, which starts when all work before it is done and shares only X
+    QLORA_TRY(launch_f8_quantize(X, QLORA_BF16, x8, s, true));
   }
-  // beside the U launch, which starts when all work before it is done and shares only X;
-  // the product starts beside both and reads W at once (8 x 4096 x 4096: 13.5 -> 11.3 us)
-  QLORA_TRY(launch_f8_quantize(X, QLORA_BF16, x8, s, true));
+  // starts beside what is ahead of it in this call and reads W at once
   return f8_gemm(x8, W, true, Y, false, F8Lora{su, B, r, true}, s);
 }
 

@@ -592,11 +592,16 @@ def _empty_in(stream, shape, dtype, device):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _workspace_in(stream, nbytes, device):
-    if stream is None:
-        return _workspace(nbytes, device)
-    with torch.cuda.stream(stream):
-        return _workspace(nbytes, device)
+def _workspace_in(stream, nbytes, device, check):
+    """The workspace of one call.  No kernel reads what it did not write there, only
+    qlora_check reads the status word: zeros cost a launch."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _workspace_in(None, nbytes, device, check)
+    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    if check:
+        ws[:256].zero_()
+    return ws
 
 
 def qlora_f8_quantize(X, layout=QLORA_F8_ROWS, format=QLORA_E4M3, pow2=False, out=None,
@@ -711,7 +716,7 @@ def qlora_linear_bwd_f8(q, A, B, r, alpha, X8, U, dY, adapter=None, p=0.0, keep_
     s = _device_stream(stream, q.codes, X8.codes, A, B, U, dY, dX, dA, dB, adapter, keep_mask,
                        workspace)
     if workspace is None:
-        workspace = _workspace_in(stream, qlora_linear_bwd_f8_workspace(M, N, K, rt), dev)
+        workspace = _workspace_in(stream, qlora_linear_bwd_f8_workspace(M, N, K, rt), dev, check)
     _ok(lib().qlora_linear_bwd_f8(q.struct, pa, pb, r, float(alpha), o, X8.struct, pu, py, px, pda,
                                   pdb, 1 if accumulate else 0, workspace.data_ptr(),
                                   workspace.numel(), s), "qlora_linear_bwd_f8")
@@ -750,7 +755,7 @@ def qlora_f8_linear_fwd(W, A, B, alpha, X, X8, Y=None, U_save=None, workspace=No
     pu = None if U_save is None else _expect("U", U_save, (M, r), torch.float32)
     s = _device_stream(stream, W.codes, A, B, X, X8.codes, Y, U_save, workspace)
     if workspace is None:
-        workspace = _workspace_in(stream, qlora_f8_linear_workspace(M, N, K, r)[0], X.device)
+        workspace = _workspace_in(stream, qlora_f8_linear_workspace(M, N, K, r)[0], X.device, check)
     _ok(lib().qlora_f8_linear_fwd(W.struct, pa, pb, r, float(alpha), px, X8.struct, py, pu,
                                   workspace.data_ptr(), workspace.numel(), s),
         "qlora_f8_linear_fwd")
@@ -774,7 +779,7 @@ def qlora_f8_linear_bwd(W, A, B, alpha, X8, U, dY, grad_format=QLORA_E5M2, dX=No
     dX, dA, dB, px, pda, pdb = _grads(M, N, K, r, dev, want_dx, dX, dA, dB, stream)
     s = _device_stream(stream, W.codes, X8.codes, A, B, U, dY, dX, dA, dB, workspace)
     if workspace is None:
-        workspace = _workspace_in(stream, qlora_f8_linear_workspace(M, N, K, r)[1], dev)
+        workspace = _workspace_in(stream, qlora_f8_linear_workspace(M, N, K, r)[1], dev, check)
     _ok(lib().qlora_f8_linear_bwd(W.struct, pa, pb, r, float(alpha), X8.struct, pu, py,
                                   int(grad_format), px, pda, pdb, 1 if accumulate else 0,
                                   workspace.data_ptr(), workspace.numel(), s),

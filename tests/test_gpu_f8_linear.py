@@ -321,3 +321,57 @@ def test_timed_and_counted():
     assert t[Q.QLORA_KERNEL_QUANTIZE][1] == 2 and t[Q.QLORA_KERNEL_LORA_GEMM][1] >= 3
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M,N,K,r", [(1, 64, 72, 8), (3, 200, 1032, 24), (9, 136, 320, 72),
+                                     (16, 128, 2048, 200), (37, 200, 328, 16),
+                                     (130, 256, 704, 40), (520, 264, 448, 136)])
+def test_workspace_holds_anything(M, N, K, r):
+    """A workspace whose bytes past the status word are NaN gives the same results: nothing is
+    read that the call did not write, padding included."""
+    W, A, B, X, dY = (t.to(DEV) for t in _rand_case(M, N, K, r, 21))
+    w8 = Q.qlora_f8_quantize(W, Q.QLORA_F8_TILES)
+    q = Q.qlora_quantize(W) if K % 64 == 0 else None
+    wf, wb = Q.qlora_f8_linear_workspace(M, N, K, r)
+    need = (wf, wb, Q.qlora_linear_bwd_f8_workspace(M, N, K, r) if q else 0)
+
+    def step(fill):
+        ws = [torch.full((max(n, 256),), fill, dtype=torch.uint8, device=DEV) for n in need]
+        for w in ws:
+            w[:256] = 0
+        x8 = Q.F8Matrix.empty(M, K)
+        U = torch.empty((M, r), dtype=torch.float32, device=DEV)
+        out = [Q.qlora_f8_linear_fwd(w8, A, B, 16.0, X, x8, U_save=U, workspace=ws[0], check=True),
+               U, *Q.qlora_f8_linear_bwd(w8, A, B, 16.0, x8, U, dY, workspace=ws[1], check=True)]
+        if q:
+            out += Q.qlora_linear_bwd_f8(q, A, B, r, 16.0, x8, U, dY, workspace=ws[2], check=True)
+        return out
+    for a, b in zip(step(0), step(0xff)):
+        assert torch.isfinite(a.float()).all() and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("M", [1, 5, 8, 9, 16])
+@pytest.mark.parametrize("K,r", [(8, 8), (136, 16), (1096, 40), (4096, 16), (11008, 64),
+                                 (20000, 256)])
+@pytest.mark.parametrize("fmt,pow2", [(Q.QLORA_E4M3, False), (Q.QLORA_E5M2, True)])
+def test_few_tokens(M, K, r, fmt, pow2):
+    """Up to 16 tokens: the codes and scales of X that qlora_f8_quantize gives, U against fp64
+    (sums of K terms: K e |x||A|^T), rows past the last token left as they were."""
+    W, A, B, X, _ = _rand_case(M, 64, K, r, M + K + r)
+    if K > 8:
+        X[M - 1, 7], X[0, K - 1] = float("inf"), float("nan")
+    X, A, B = X.to(DEV), A.to(DEV), B.to(DEV)
+    w8 = Q.qlora_f8_quantize(W.to(DEV), Q.QLORA_F8_TILES)
+    want = Q.qlora_f8_quantize(X, Q.QLORA_F8_ROWS, fmt, pow2)
+    full = Q.F8Matrix.empty(M + 3, K, format=fmt, pow2=pow2)
+    full.codes.fill_(77)
+    x8 = Q.F8Matrix(M, K, Q.QLORA_F8_ROWS, fmt, pow2, full.codes[:M], torch.empty_like(want.scales))
+    U = torch.full((M + 1, r), 5.0, device=DEV)
+    Q.qlora_f8_linear_fwd(w8, A, B, 16.0, X, x8, U_save=U[:M], check=True)
+    assert torch.equal(x8.codes, want.codes) and torch.equal(x8.scales, want.scales)
+    assert (full.codes[M:] == 77).all() and (U[M:] == 5).all()
+    x, a = _f(X), _f(A)
+    bad = ~np.isfinite(x).all(axis=1)
+    assert (~torch.isfinite(U[:M]).cpu().numpy())[bad].all()
+    x = x[~bad]
+    _within(U[:M].cpu()[torch.from_numpy(~bad)], x @ a.T, K * E * np.abs(x) @ np.abs(a).T, "U")
