@@ -23,9 +23,10 @@ qlora_status launch_f8_quantize(const void* X, int32_t x_dtype, const qlora_f8& 
 qlora_status launch_f8_dequantize(const qlora_f8& q, void* out, int32_t out_dtype,
                                   cudaStream_t s);
 
-// f8_front.cu: for up to 16 tokens of bf16 X, 8 bits of X (by rows) and U = X A^T in one
-// launch: U (M x r fp32, or NULL) and su = sc U as bf16 [hi | lo], lora_span(r) columns
-// each.  d_in a multiple of 8.
+// f8_front.cu: 8 bits of bf16 X (by rows) and U = X A^T in one launch: U (M x r fp32, or
+// NULL) and su = sc U as bf16 [hi | lo], lora_span(r) columns each.  d_in a multiple of 8.
+// f8_front_takes: where it is the faster form.
+bool f8_front_takes(int64_t M, int64_t K, int32_t r);
 qlora_status f8_front(const void* X, const qlora_f8& x8, const void* A, int32_t r, float sc,
                       float* U, void* su, cudaStream_t s);
 

@@ -1,9 +1,9 @@
-// What the 8-bit layer needs of X before its product, for up to 16 tokens, in one
-// launch: X in 8 bits by rows (definitions: f8_quantize.cu) and the LoRA factor
+// What the 8-bit layer needs of X before its product, for up to a few hundred tokens, in
+// one launch: X in 8 bits by rows (definitions: f8_quantize.cu) and the LoRA factor
 //   U[m][j] = sum_k X[m][k] A[j][k],
 // as fp32 and as the product's operand, s U in bf16 [hi | lo].
 //
-// A warp takes a block of 128 columns: its tokens (one 16-byte load per row and 32
+// A warp takes a block of 128 columns of 16 tokens (one 16-byte load per row and 32
 // columns and lane) and 16 ranks' rows of A, all loads before the first use.  The same
 // registers give the block's scale (two shuffles across the four lanes of a row), its
 // codes, and the operands of the matrix instructions: a lane's 8 consecutive columns
@@ -13,11 +13,11 @@
 //
 // Bound by latency: one load from HBM or L2, the sum across the cluster and the launch.
 // Forward of the layer, per call in a sequence, against the two launches of the NF4
-// layer's rank product and the quantiser: 8 x 4096 x 11008 at rank 64 in 14.5 us (19.3),
-// 16 x 8192 x 8192 in 19.3 (23.8), 8 x 4096 x 4096 at rank 16 in 10.6 (11.3), one token
+// layer's rank product and the quantiser: 8 x 4096 x 11008 at rank 64 in 14.3 us (19.3),
+// 16 x 8192 x 8192 in 18.3 (23.8), 8 x 4096 x 4096 at rank 16 in 10.1 (11.3), one token
 // of it in 9.5 (9.2); the product alone takes 11.5, 14.8, 7.4 and 6.5.
-// (16 tokens x 64 ranks are 16 x 64 x K products; mma.sync does them between the
-// loads' arrivals, where tcgen05 would need operands in shared memory first.)
+// (16 tokens x 16 ranks x 128 columns are 16 matrix instructions of mma.sync, done
+// between the loads' arrivals; tcgen05 would need the operands in shared memory first.)
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -38,8 +38,9 @@ struct FrontArgs {
   const __nv_bfloat16* a;  // r x K
   uint8_t* codes;
   float* scales;           // [kb][M]
-  int64_t k, ld;
-  int32_t m, r, kbs, per;  // 128-column blocks, blocks per CTA
+  int64_t k, ld, m;
+  int32_t r, kbs, per;     // 128-column blocks, blocks per CTA
+  int32_t tiles;           // 16-token tiles per CTA (warps w, w + tiles, ... share one)
   int32_t pow2, span;
   float* u;                // M x r or NULL
   __nv_bfloat16* su;       // M x [span | span]
@@ -59,21 +60,27 @@ __device__ __forceinline__ float word_value(uint32_t w, int half) {
   return __uint_as_float(half ? (w & 0xffff0000u) : (w << 16));
 }
 
-// TWO: more than 8 tokens (a lane holds rows g and g + 8)
+// TWO: more than 8 tokens (a lane holds rows g and g + 8).
 template <bool E5M2, bool TWO>
 __global__ void __launch_bounds__(32 * kMaxWarps) f8_front_kernel(const FrontArgs p) {
   // the product may start: it reads what this launch writes after its own wait
   ptx::grid_launch_dependents();
   constexpr int kHalves = TWO ? 2 : 1;
   __shared__ float red[kMaxWarps][16][kRanks + 1];
-  __shared__ float part[16][kRanks];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
+  const int tile = warp % p.tiles, slice = warp / p.tiles;
+  const int slices = static_cast<int>(blockDim.x >> 5) / p.tiles;
+  const int64_t tile0 = static_cast<int64_t>(blockIdx.z) * p.tiles;
+  const int64_t row0 = 16 * (tile0 + tile);
   const int j0 = blockIdx.y * kRanks;
   const int kb_end = min(static_cast<int>(blockIdx.x + 1) * p.per, p.kbs);
   const int64_t k16 = (p.k + 15) / 16 * 16;
   float acc[2][4] = {};
-  for (int kb = blockIdx.x * p.per + warp; kb < kb_end; kb += warps) {
+  for (int kb = blockIdx.x * p.per + slice; kb < kb_end; kb += slices) {
+    // the CTAs of the rank blocks share the encoding; those past the last rank only encode
+    const bool encode = kb % gridDim.y == blockIdx.y;
+    if (j0 >= p.r && !encode) continue;
     const int64_t k0 = static_cast<int64_t>(kb) * 128 + 8 * t;
     uint32_t x[kHalves][16], a[2][16];  // 4 x 8 columns
 #pragma unroll
@@ -82,8 +89,8 @@ __global__ void __launch_bounds__(32 * kMaxWarps) f8_front_kernel(const FrontArg
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
         uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        if (k < p.k && g + 8 * h < p.m)
-          v = __ldg(reinterpret_cast<const uint4*>(p.x + (g + 8 * h) * p.k + k));
+        if (k < p.k && row0 + g + 8 * h < p.m)
+          v = __ldg(reinterpret_cast<const uint4*>(p.x + (row0 + g + 8 * h) * p.k + k));
         x[h][4 * i] = v.x;
         x[h][4 * i + 1] = v.y;
         x[h][4 * i + 2] = v.z;
@@ -106,11 +113,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps) f8_front_kernel(const FrontArg
       for (int n = 0; n < 2; ++n)
         mma_bf16(acc[n], x[0][i], TWO ? x[kHalves - 1][i] : 0u, x[0][i + 1],
                  TWO ? x[kHalves - 1][i + 1] : 0u, a[n][i], a[n][i + 1]);
-    // the CTAs of the rank blocks share the encoding
-    if (kb % gridDim.y != blockIdx.y) continue;
+    if (!encode) continue;
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
-      const int row = g + 8 * h;
+      const int64_t row = row0 + g + 8 * h;
       float m = amax_words<__nv_bfloat16>(x[h]);
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -139,43 +145,59 @@ __global__ void __launch_bounds__(32 * kMaxWarps) f8_front_kernel(const FrontArg
 #pragma unroll
     for (int q = 0; q < 4; ++q) red[warp][g + 8 * (q >> 1)][8 * n + 2 * t + (q & 1)] = acc[n][q];
   __syncthreads();
-  for (int e = threadIdx.x; e < 16 * kRanks; e += blockDim.x) {
-    const int m = e / kRanks, j = e % kRanks;
-    float v = 0.0f;
-    for (int w = 0; w < warps; ++w) v += red[w][m][j];
-    part[m][j] = v;
+  const int64_t left = p.m - 16 * tile0;
+  const int rows = static_cast<int>(left < 16 * p.tiles ? left : 16 * p.tiles);
+  if (slices > 1) {
+    for (int e = threadIdx.x; e < rows * kRanks; e += blockDim.x) {
+      const int m = e / kRanks, j = e % kRanks;
+      float v = red[m >> 4][m & 15][j];
+      for (int w = 1; w < slices; ++w) v += red[(m >> 4) + w * p.tiles][m & 15][j];
+      red[m >> 4][m & 15][j] = v;
+    }
   }
   ptx::cluster_sync();
   const int ctas = static_cast<int>(gridDim.x);  // the cluster spans x
   for (int e = static_cast<int>(ptx::cluster_ctarank()) + ctas * static_cast<int>(threadIdx.x);
-       e < p.m * kRanks; e += ctas * static_cast<int>(blockDim.x)) {
+       e < rows * kRanks; e += ctas * static_cast<int>(blockDim.x)) {
     const int m = e / kRanks, j = j0 + e % kRanks;
+    const float* at = &red[m >> 4][m & 15][e % kRanks];
     float y[kMaxCtas];
 #pragma unroll
     for (int q = 0; q < kMaxCtas; ++q)
-      y[q] = q < ctas ? ptx::ld_cluster_f32(ptx::cluster_addr(&part[m][e % kRanks], q)) : 0.0f;
+      y[q] = q < ctas ? ptx::ld_cluster_f32(ptx::cluster_addr(at, q)) : 0.0f;
     float v = 0.0f;
 #pragma unroll
     for (int q = 0; q < kMaxCtas; ++q)
       if (q < ctas) v += y[q];
-    if (j < p.r && p.u) p.u[static_cast<int64_t>(m) * p.r + j] = v;
+    const int64_t row = 16 * tile0 + m;
+    if (j < p.r && p.u) p.u[row * p.r + j] = v;
     if (j < p.span) {  // zeros past the last rank
       const float f = j < p.r ? p.sc * v : 0.0f;
       const __nv_bfloat16 hi = __float2bfloat16_rn(f);
-      __nv_bfloat16* o = p.su + static_cast<int64_t>(m) * 2 * p.span + j;
+      __nv_bfloat16* o = p.su + row * 2 * p.span + j;
       o[0] = hi;
       o[p.span] = j < p.r ? __float2bfloat16_rn(f - __bfloat162float(hi)) : hi;
     }
   }
-  ptx::cluster_sync();  // the others may still read part
+  ptx::cluster_sync();  // the others may still read red
 }
 
 }  // namespace
 
+// Where every warp has one block at most (16 tokens x 16 ranks x 128 columns) the launch is
+// one latency: 24 x 4096 x 4096 at rank 16 in 11.7 us, 20.0 with the tensor-core rank
+// product and the quantiser; 128 x 4096 x 4096 at rank 64 in 15.9 (19.9); 256 of them in
+// 18.6 (21.8).  With more blocks (256 x 8192 x 8192 at rank 64: 42.6, 36.7) or tokens (512 x
+// 4096 x 4096 at rank 16: 27.3, 23.0) reading X and A once each wins.
+bool f8_front_takes(int64_t M, int64_t K, int32_t r) {
+  return M <= 16 ||
+         (M <= 256 && ceil_div(M, 16) * f8_blocks(K) * ceil_div(r, kRanks) <= 148 * kMaxWarps);
+}
+
 qlora_status f8_front(const void* X, const qlora_f8& x8, const void* A, int32_t r, float sc,
                       float* U, void* su, cudaStream_t s) {
   const int64_t M = x8.rows, K = x8.cols;
-  if (M < 1 || M > kSmallM || K % 8 != 0) return QLORA_ERR_UNSUPPORTED;
+  if (M < 1 || K % 8 != 0) return QLORA_ERR_UNSUPPORTED;
   FrontArgs p{};
   p.x = static_cast<const __nv_bfloat16*>(X);
   p.a = static_cast<const __nv_bfloat16*>(A);
@@ -183,7 +205,7 @@ qlora_status f8_front(const void* X, const qlora_f8& x8, const void* A, int32_t 
   p.scales = x8.scales;
   p.k = K;
   p.ld = x8.ld;
-  p.m = static_cast<int32_t>(M);
+  p.m = M;
   p.r = r;
   p.kbs = static_cast<int32_t>(f8_blocks(K));
   p.pow2 = x8.pow2;
@@ -193,10 +215,20 @@ qlora_status f8_front(const void* X, const qlora_f8& x8, const void* A, int32_t 
   p.sc = sc;
   p.per = static_cast<int32_t>(ceil_div(p.kbs, kMaxCtas));
   const int ctas = static_cast<int>(ceil_div(p.kbs, p.per));
+  const int64_t groups = p.span / kRanks;  // those past the last rank write zeros
+  // a warp per 16 tokens and block of 128 columns, as far as all run at once; then
+  // more tokens per CTA and more blocks per warp
+  int64_t blocks;
+  int slices;
+  for (p.tiles = 1;; p.tiles *= 2) {
+    blocks = ceil_div(M, 16 * p.tiles);
+    slices = std::min(kMaxWarps / p.tiles, p.per);
+    if (p.tiles == 8 || ctas * groups * blocks * p.tiles * slices <= 148 * kMaxWarps) break;
+  }
   cudaLaunchConfig_t cfg = {};
-  // the rank blocks up to the span: those past the last rank write its zeros
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(ceil_div(p.span, kRanks)));
-  cfg.blockDim = dim3(static_cast<unsigned>(32 * std::min(kMaxWarps, p.per)));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(groups),
+                     static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * p.tiles * slices));
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -66,7 +66,7 @@ qlora_status f8_linear_forward(const qlora_f8& W, const void* A, const void* B, 
   auto* st = reinterpret_cast<DeviceStatus*>(ws);
   char* su = ws + L.su;
   // U = X A^T -> U_save (fp32) and sU = s U as bf16 hi + lo
-  if (M <= kSmallM) {
+  if (f8_front_takes(M, K, r)) {
     QLORA_TRY(f8_front(X, x8, A, r, sc, U_save, su, s));  // and the 8 bits of X
   } else {
     ReduceArgs ra = reduce_args(nullptr, 1, M, r, r16);

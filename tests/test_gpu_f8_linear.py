@@ -350,12 +350,13 @@ def test_workspace_holds_anything(M, N, K, r):
         assert torch.isfinite(a.float()).all() and torch.equal(a, b)
 
 
-@pytest.mark.parametrize("M", [1, 5, 8, 9, 16])
-@pytest.mark.parametrize("K,r", [(8, 8), (136, 16), (1096, 40), (4096, 16), (11008, 64),
-                                 (20000, 256)])
+@pytest.mark.parametrize("M,K,r", [(m, k, r) for m in (1, 5, 8, 9, 16) for k, r in (
+    (8, 8), (136, 16), (1096, 40), (4096, 16), (11008, 64), (20000, 256))]
+    + [(17, 8, 8), (33, 1096, 40), (100, 4096, 16), (250, 4096, 64), (256, 264, 256),
+       (129, 2048, 136), (257, 128, 8), (40, 20000, 256)])
 @pytest.mark.parametrize("fmt,pow2", [(Q.QLORA_E4M3, False), (Q.QLORA_E5M2, True)])
 def test_few_tokens(M, K, r, fmt, pow2):
-    """Up to 16 tokens: the codes and scales of X that qlora_f8_quantize gives, U against fp64
+    """Up to some hundred tokens: the codes and scales of X that qlora_f8_quantize gives, U against fp64
     (sums of K terms: K e |x||A|^T), rows past the last token left as they were."""
     W, A, B, X, _ = _rand_case(M, 64, K, r, M + K + r)
     if K > 8:
