@@ -101,12 +101,24 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
   float* v = reinterpret_cast<float*>(vt);  // few tokens: V in fp32
   float* part = reinterpret_cast<float*>(ws + L.part);
   const bool small = M <= kSmallM;
+  const qlora_f8 dy8{M, N, L.dy_ld, QLORA_F8_ROWS, grad_format, x8.pow2, 0,
+                     reinterpret_cast<uint8_t*>(ws + L.dy_codes),
+                     reinterpret_cast<float*>(ws + L.dy_scales)};
+  // dX on the caller's stream; beside it dB, which needs only inputs, and dA after V
+  SideStream* ss = nullptr;
+  QLORA_TRY(side_stream(&ss));
+  const cudaStream_t s2 = ss->stream;
+  auto fork = [&]() -> bool {
+    return cudaEventRecord(ss->fork, s) == cudaSuccess &&
+           cudaStreamWaitEvent(s2, ss->fork, 0) == cudaSuccess;
+  };
   // V = dY B -> sV = s V as [hi | lo], and V (fp32) or V^T as [hi ; lo]
-  if (small) {
-    const RankOut rv{r, v, r, 1.0f, reinterpret_cast<__nv_bfloat16*>(sv), 2 * span,
-                     sc, span, nullptr, r};
-    QLORA_TRY(rank_v(dY, B, static_cast<int>(M), N, span, rv, s));
-  } else {
+  auto v_work = [&]() -> qlora_status {
+    if (small) {
+      const RankOut rv{r, v, r, 1.0f, reinterpret_cast<__nv_bfloat16*>(sv), 2 * span,
+                       sc, span, nullptr, r};
+      return rank_v(dY, B, static_cast<int>(M), N, span, rv, s);
+    }
     ReduceArgs ra = reduce_args(nullptr, 1, M, r, r16);
     ra.o2 = sv;
     ra.ld2 = 2 * span;
@@ -117,30 +129,10 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
     ra.ld3 = mp;
     ra.a3 = 1.0f;
     ra.o3_lo = r16;
-    QLORA_TRY(tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s));
-  }
-  const qlora_f8 dy8{M, N, L.dy_ld, QLORA_F8_ROWS, grad_format, x8.pow2, 0,
-                     reinterpret_cast<uint8_t*>(ws + L.dy_codes),
-                     reinterpret_cast<float*>(ws + L.dy_scales)};
-  // beside the V launch, which shares only dY
-  if (dX) QLORA_TRY(launch_f8_quantize(dY, QLORA_BF16, dy8, s, true));
-  // dB and dA on the side stream, dX on the caller's: they share only inputs
-  SideStream* ss = nullptr;
-  QLORA_TRY(side_stream(&ss));
-  const cudaStream_t s2 = ss->stream;
-  if (cudaEventRecord(ss->fork, s) != cudaSuccess ||
-      cudaStreamWaitEvent(s2, ss->fork, 0) != cudaSuccess)
-    return QLORA_ERR_CUDA;
-  auto main_work = [&]() -> qlora_status {
-    if (!dX) return QLORA_OK;
-    return f8_gemm(dy8, W, false, dX, false, F8Lora{sv, A, r, true}, s);
+    return tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s);
   };
-  auto side_work = [&]() -> qlora_status {
-    if (small) {
-      const int m = static_cast<int>(M);
-      QLORA_TRY(small_grad_b(dY, U, m, N, r, sc, accumulate, dB, s2));
-      return f8_small_grad_a(v, x8, r, sc, accumulate, dA, s2);
-    }
+  auto grad_b = [&]() -> qlora_status {
+    if (small) return small_grad_b(dY, U, static_cast<int>(M), N, r, sc, accumulate, dB, s2);
     QLORA_TRY(transpose_to_bf16(U, true, M, r, r, ut, mp, r16, s2));
     ReduceArgs rb = reduce_args(part, L.split_db, N, r, 2 * r16);
     rb.lo = r16;
@@ -148,17 +140,24 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
     rb.ld1 = r;
     rb.a1 = sc;
     rb.acc1 = accumulate;
-    QLORA_TRY(rank_product(dY, true, N, M, N, ut, mp, 2 * r16, 2 * r16, part, L.split_db, rb, st,
-                           s2));
+    return rank_product(dY, true, N, M, N, ut, mp, 2 * r16, 2 * r16, part, L.split_db, rb, st, s2);
+  };
+  auto all_work = [&]() -> qlora_status {
+    QLORA_TRY(v_work());
+    // beside the V launch, which shares only dY
+    if (dX) QLORA_TRY(launch_f8_quantize(dY, QLORA_BF16, dy8, s, true));
+    QLORA_TRY(grad_b());
+    if (!fork()) return QLORA_ERR_CUDA;
+    if (dX) QLORA_TRY(f8_gemm(dy8, W, false, dX, false, F8Lora{sv, A, r, true}, s));
+    if (small) return f8_small_grad_a(v, x8, r, sc, accumulate, dA, s2);
     return f8_grad_a(vt, mp, x8, r, sc, accumulate, dA, st, s2);
   };
-  const qlora_status st_main = main_work();
-  const qlora_status st_side = side_work();
+  if (!fork()) return QLORA_ERR_CUDA;
+  const qlora_status done = all_work();
   // join on every path, so that nothing of this call runs past it on the side stream
   const bool joined = cudaEventRecord(ss->join, s2) == cudaSuccess &&
                       cudaStreamWaitEvent(s, ss->join, 0) == cudaSuccess;
-  if (st_side != QLORA_OK) return st_side;
-  if (st_main != QLORA_OK) return st_main;
+  if (done != QLORA_OK) return done;
   return joined ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
