@@ -23,12 +23,24 @@ qlora_status launch_f8_quantize(const void* X, int32_t x_dtype, const qlora_f8& 
 qlora_status launch_f8_dequantize(const qlora_f8& q, void* out, int32_t out_dtype,
                                   cudaStream_t s);
 
-// f8_front.cu: 8 bits of bf16 X (by rows) and U = X A^T in one launch: U (M x r fp32, or
-// NULL) and su = sc U as bf16 [hi | lo], lora_span(r) columns each.  d_in a multiple of 8.
+// f8_front.cu: 8 bits of bf16 X (into x8, by rows) and one LoRA factor in one launch:
+// U = X A^T with A r x K, or (along) U = X A with A K x r.  K = x8.cols, r multiples of 8.
 // f8_front_takes: where it is the faster form.
+struct FrontOp {
+  const void* x;
+  const void* a;
+  int32_t r;
+  bool along;
+  bool encode;    // false: x8 gives the sizes only
+  float* u;       // U (M x r fp32) or NULL
+  float sc;
+  void* su;       // sc U as bf16 [hi | lo], lora_span(r) columns each
+  void* ut;       // U^T as bf16 [hi ; lo], lo from row ut_lo on, rows of ut_ld; or NULL
+  int64_t ut_ld;
+  int32_t ut_lo;
+};
 bool f8_front_takes(int64_t M, int64_t K, int32_t r);
-qlora_status f8_front(const void* X, const qlora_f8& x8, const void* A, int32_t r, float sc,
-                      float* U, void* su, cudaStream_t s);
+qlora_status f8_front(const FrontOp& f, const qlora_f8& x8, cudaStream_t s);
 
 // The LoRA term of a product, added as extra stages of the same accumulators:
 // C += hi . R + lo . R with [hi | lo] = L (m x 2 lora_span(r) bf16) and R (bf16)

@@ -48,7 +48,7 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
 template <typename T, int N>
 __device__ __forceinline__ float amax_words(const uint32_t (&w)[N]) {
   float a = 0.0f;
-  if (sizeof(T) == 2) {
+  if constexpr (sizeof(T) == 2) {
     __nv_bfloat162 m = __floats2bfloat162_rn(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < N; ++j)
@@ -60,10 +60,10 @@ __device__ __forceinline__ float amax_words(const uint32_t (&w)[N]) {
     for (int j = 0; j < N; ++j)
       a = fmaxf(a, fmaxf(finite_abs(__uint_as_float(w[j] << 16)),
                          finite_abs(__uint_as_float(w[j] & 0xffff0000u))));
-    return a;
-  }
+  } else {
 #pragma unroll
-  for (int j = 0; j < N; ++j) a = fmaxf(a, finite_abs(__uint_as_float(w[j])));
+    for (int j = 0; j < N; ++j) a = fmaxf(a, finite_abs(__uint_as_float(w[j])));
+  }
   return a;
 }
 

@@ -67,7 +67,8 @@ qlora_status f8_linear_forward(const qlora_f8& W, const void* A, const void* B, 
   char* su = ws + L.su;
   // U = X A^T -> U_save (fp32) and sU = s U as bf16 hi + lo
   if (f8_front_takes(M, K, r)) {
-    QLORA_TRY(f8_front(X, x8, A, r, sc, U_save, su, s));  // and the 8 bits of X
+    const FrontOp f{X, A, r, false, true, U_save, sc, su, nullptr, 0, 0};
+    QLORA_TRY(f8_front(f, x8, s));  // and the 8 bits of X
   } else {
     ReduceArgs ra = reduce_args(nullptr, 1, M, r, r16);
     ra.o1 = U_save;
@@ -112,12 +113,12 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
     return cudaEventRecord(ss->fork, s) == cudaSuccess &&
            cudaStreamWaitEvent(s2, ss->fork, 0) == cudaSuccess;
   };
-  // V = dY B -> sV = s V as [hi | lo], and V (fp32) or V^T as [hi ; lo]
+  // V = dY B -> sV = s V as [hi | lo], and V (fp32) or V^T as [hi ; lo]; the 8 bits of dY
   auto v_work = [&]() -> qlora_status {
-    if (small) {
-      const RankOut rv{r, v, r, 1.0f, reinterpret_cast<__nv_bfloat16*>(sv), 2 * span,
-                       sc, span, nullptr, r};
-      return rank_v(dY, B, static_cast<int>(M), N, span, rv, s);
+    if (f8_front_takes(M, N, r)) {
+      const FrontOp f{dY, B, r, true, dX != nullptr, small ? v : nullptr, sc, sv,
+                      small ? nullptr : vt, mp, r16};
+      return f8_front(f, dy8, s);
     }
     ReduceArgs ra = reduce_args(nullptr, 1, M, r, r16);
     ra.o2 = sv;
@@ -129,7 +130,9 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
     ra.ld3 = mp;
     ra.a3 = 1.0f;
     ra.o3_lo = r16;
-    return tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s);
+    QLORA_TRY(tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s));
+    // beside the V launch, which shares only dY
+    return dX ? launch_f8_quantize(dY, QLORA_BF16, dy8, s, true) : QLORA_OK;
   };
   auto grad_b = [&]() -> qlora_status {
     if (small) return small_grad_b(dY, U, static_cast<int>(M), N, r, sc, accumulate, dB, s2);
@@ -144,8 +147,6 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
   };
   auto all_work = [&]() -> qlora_status {
     QLORA_TRY(v_work());
-    // beside the V launch, which shares only dY
-    if (dX) QLORA_TRY(launch_f8_quantize(dY, QLORA_BF16, dy8, s, true));
     QLORA_TRY(grad_b());
     if (!fork()) return QLORA_ERR_CUDA;
     if (dX) QLORA_TRY(f8_gemm(dy8, W, false, dX, false, F8Lora{sv, A, r, true}, s));
