@@ -511,6 +511,11 @@ def qlora_f8_sizes(rows, cols, layout=QLORA_F8_ROWS):
     return {"ld": ld.value, "codes": codes.value, "scales": scales.value}
 
 
+def _rows_of(shape, dtype, device):
+    """torch.empty of a 2-D shape, in half its time on the host."""
+    return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+
+
 def _f8_scales_shape(rows, cols, layout):
     kb = -(-cols // 128)
     return (kb, rows) if layout == QLORA_F8_ROWS else (-(-rows // 128), kb)
@@ -554,9 +559,8 @@ class F8Matrix:
         m = cls.__new__(cls)
         ld = (cols + 15) // 16 * 16
         m._set(rows, cols, layout, format, pow2,
-               torch.empty((rows, ld), dtype=torch.uint8, device=device),
-               torch.empty(_f8_scales_shape(rows, cols, layout), dtype=torch.float32,
-                           device=device), ld)
+               _rows_of((rows, ld), torch.uint8, device),
+               _rows_of(_f8_scales_shape(rows, cols, layout), torch.float32, device), ld)
         return m
 
     @property
@@ -575,7 +579,7 @@ def _device_stream(stream, *tensors):
     live elsewhere are refused."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
@@ -587,9 +591,9 @@ def _device_stream(stream, *tensors):
 def _empty_in(stream, shape, dtype, device):
     """A tensor for work on `stream`: its memory is reused in that stream's order."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _rows_of(shape, dtype, device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _rows_of(shape, dtype, device)
 
 
 def _workspace_in(stream, nbytes, device, check):
@@ -598,7 +602,7 @@ def _workspace_in(stream, nbytes, device, check):
     if stream is not None:
         with torch.cuda.stream(stream):
             return _workspace_in(None, nbytes, device, check)
-    ws = torch.empty(max(int(nbytes), 256), dtype=torch.uint8, device=device)
+    ws = torch.empty_strided((max(int(nbytes), 256),), (1,), dtype=torch.uint8, device=device)
     if check:
         ws[:256].zero_()
     return ws
