@@ -15,11 +15,8 @@ inline int64_t f8_blocks(int64_t n) { return ceil_div(n, 128); }
 // abi_f8.cu: shape and pointer checks of a qlora_f8.
 qlora_status check_f8(const qlora_f8& q);
 
-// f8_quantize.cu.  beside_last: the launch may run beside the one before it in the
-// stream (a programmatic dependent launch that waits for nothing): only where that
-// one reads and writes none of q's arrays and does not write X.
-qlora_status launch_f8_quantize(const void* X, int32_t x_dtype, const qlora_f8& q, cudaStream_t s,
-                                bool beside_last = false);
+// f8_quantize.cu
+qlora_status launch_f8_quantize(const void* X, int32_t x_dtype, const qlora_f8& q, cudaStream_t s);
 qlora_status launch_f8_dequantize(const qlora_f8& q, void* out, int32_t out_dtype,
                                   cudaStream_t s);
 
@@ -41,6 +38,9 @@ struct FrontOp {
 };
 bool f8_front_takes(int64_t M, int64_t K, int32_t r);
 qlora_status f8_front(const FrontOp& f, const qlora_f8& x8, cudaStream_t s);
+// f8_front_wide.cu: the same for many tokens; encode has to be set.
+qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* st,
+                           cudaStream_t s);
 
 // The LoRA term of a product, added as extra stages of the same accumulators:
 // C += hi . R + lo . R with [hi | lo] = L (m x 2 lora_span(r) bf16) and R (bf16)

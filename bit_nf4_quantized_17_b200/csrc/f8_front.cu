@@ -6,10 +6,10 @@
 namespace qlora {
 
 // Where every warp has one block at most (16 tokens x 16 ranks x 128 columns) the launch is
-// one latency: 24 x 4096 x 4096 at rank 16 in 11.7 us, 20.0 with the tensor-core rank
-// product and the quantiser; 128 x 4096 x 4096 at rank 64 in 15.9 (19.9); 256 of them in
-// 18.6 (21.8).  With more blocks (256 x 8192 x 8192 at rank 64: 42.6, 36.7) or tokens (512 x
-// 4096 x 4096 at rank 16: 27.3, 23.0) reading X and A once each wins.
+// one latency.  Forward of the layer with this kernel and with f8_front_wide's: 24 x 4096 x
+// 4096 at rank 16 11.7 and 14.6 us, 128 of them at rank 64 16.3 and 18.6, 256 18.9 and
+// 20.4.  With more blocks (256 x 8192 x 8192 at rank 64: 42.6 and 36.8) or tokens (512 x
+// 4096 x 4096 at rank 16: 27.3 and 22) reading X and A once each wins.
 bool f8_front_takes(int64_t M, int64_t K, int32_t r) {
   return M <= 16 ||
          (M <= 256 && ceil_div(M, 16) * f8_blocks(K) * ceil_div(r, kRanks) <= 148 * kMaxWarps);

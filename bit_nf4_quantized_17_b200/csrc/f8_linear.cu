@@ -66,23 +66,9 @@ qlora_status f8_linear_forward(const qlora_f8& W, const void* A, const void* B, 
   auto* st = reinterpret_cast<DeviceStatus*>(ws);
   char* su = ws + L.su;
   // U = X A^T -> U_save (fp32) and sU = s U as bf16 hi + lo
-  if (f8_front_takes(M, K, r)) {
-    const FrontOp f{X, A, r, false, true, U_save, sc, su, nullptr, 0, 0};
-    QLORA_TRY(f8_front(f, x8, s));  // and the 8 bits of X
-  } else {
-    ReduceArgs ra = reduce_args(nullptr, 1, M, r, r16);
-    ra.o1 = U_save;
-    ra.ld1 = r;
-    ra.a1 = 1.0f;
-    ra.o2 = su;
-    ra.ld2 = 2 * span;
-    ra.a2 = sc;
-    ra.o2_lo = span;
-    ra.o2_pad = 1;
-    QLORA_TRY(tc_rank_gemm(X, false, M, K, K, A, false, K, r, r16, ra, st, s));
-    // beside the U launch, which starts when all work before it is done and shares only X
-    QLORA_TRY(launch_f8_quantize(X, QLORA_BF16, x8, s, true));
-  }
+  // and the 8 bits of X
+  const FrontOp f{X, A, r, false, true, U_save, sc, su, nullptr, 0, 0};
+  QLORA_TRY(f8_front_takes(M, K, r) ? f8_front(f, x8, s) : f8_front_wide(f, x8, st, s));
   // starts beside what is ahead of it in this call and reads W at once
   return f8_gemm(x8, W, true, Y, false, F8Lora{su, B, r, true}, s);
 }
@@ -115,11 +101,10 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
   };
   // V = dY B -> sV = s V as [hi | lo], and V (fp32) or V^T as [hi ; lo]; the 8 bits of dY
   auto v_work = [&]() -> qlora_status {
-    if (f8_front_takes(M, N, r)) {
-      const FrontOp f{dY, B, r, true, dX != nullptr, small ? v : nullptr, sc, sv,
-                      small ? nullptr : vt, mp, r16};
-      return f8_front(f, dy8, s);
-    }
+    const FrontOp f{dY, B, r, true, dX != nullptr, small ? v : nullptr, sc, sv,
+                    small ? nullptr : vt, mp, r16};
+    if (f8_front_takes(M, N, r)) return f8_front(f, dy8, s);
+    if (dX) return f8_front_wide(f, dy8, st, s);
     ReduceArgs ra = reduce_args(nullptr, 1, M, r, r16);
     ra.o2 = sv;
     ra.ld2 = 2 * span;
@@ -130,9 +115,7 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
     ra.ld3 = mp;
     ra.a3 = 1.0f;
     ra.o3_lo = r16;
-    QLORA_TRY(tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s));
-    // beside the V launch, which shares only dY
-    return dX ? launch_f8_quantize(dY, QLORA_BF16, dy8, s, true) : QLORA_OK;
+    return tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s);
   };
   auto grad_b = [&]() -> qlora_status {
     if (small) return small_grad_b(dY, U, static_cast<int>(M), N, r, sc, accumulate, dB, s2);

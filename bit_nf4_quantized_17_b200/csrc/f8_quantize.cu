@@ -105,12 +105,6 @@ __device__ __forceinline__ void store16(const L& v, float inv, const QArgs& p, i
   *reinterpret_cast<uint4*>(p.codes + row * p.ld + c0) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
-// Where the launch may run beside the one before it, it still ends after it: what
-// follows in the stream waits for both.  (Without that attribute it returns at once.)
-__device__ __forceinline__ void end_beside_last() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // A scale per row and 128 columns.  A warp takes 512 consecutive columns of a
 // row (8 lanes per block: the maximum is 3 shuffles), a CTA ROWS rows of them;
 // its scales leave through shared memory, so that a block column's scales of
@@ -149,7 +143,6 @@ __global__ void __launch_bounds__(kThreads) f8_rows_kernel(const QArgs p) {
     if (kbg * 4 + b < p.kb && row0 + i < p.rows)
       p.scales[(kbg * 4 + b) * p.rows + row0 + i] = sc[b][i];
   }
-  end_beside_last();
 }
 
 // 16 bytes of values of a row from column c0 (8 bf16 or 4 fp32), zeros past the last
@@ -234,7 +227,6 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) f8_tiles_ker
     }
   }
   if (threadIdx.x == 0) p.scales[rb * p.kb + kb] = s;
-  end_beside_last();
 }
 
 template <bool E5M2>
@@ -323,34 +315,22 @@ __global__ void __launch_bounds__(kThreads) f8_restore_kernel(const QArgs p, T* 
 }
 
 template <typename T, bool E5M2, bool VEC>
-qlora_status quantize_as(const QArgs& p, bool tiles, bool beside_last, cudaStream_t s) {
+qlora_status quantize_as(const QArgs& p, bool tiles, cudaStream_t s) {
   const int64_t groups = (p.kb + 3) / 4;
   // 8 rows a CTA while 32 would leave SMs without work
   const bool few = ceil_div(p.rows, 32) * groups < 296;
   const int64_t grid = tiles ? p.kb * f8_blocks(p.rows) : groups * ceil_div(p.rows, few ? 8 : 32);
   if (grid > 0x7fffffff) return QLORA_ERR_SHAPE;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = beside_last ? 1 : 0;
+  const unsigned g = static_cast<unsigned>(grid);
   count_launch();
   timing_mark(QLORA_KERNEL_QUANTIZE, s, true);
-  const cudaError_t e =
-      cudaLaunchKernelEx(&cfg,
-                         tiles ? f8_tiles_kernel<T, E5M2, VEC>
-                         : few ? f8_rows_kernel<T, E5M2, VEC, 8>
-                               : f8_rows_kernel<T, E5M2, VEC, 32>,
-                         p);
+  if (tiles)
+    f8_tiles_kernel<T, E5M2, VEC><<<g, kThreads, 0, s>>>(p);
+  else if (few)
+    f8_rows_kernel<T, E5M2, VEC, 8><<<g, kThreads, 0, s>>>(p);
+  else
+    f8_rows_kernel<T, E5M2, VEC, 32><<<g, kThreads, 0, s>>>(p);
   timing_mark(QLORA_KERNEL_QUANTIZE, s, false);
-  if (e != cudaSuccess) {
-    (void)cudaGetLastError();
-    return QLORA_ERR_CUDA;
-  }
   return after_launch("f8_quantize", s);
 }
 
@@ -374,23 +354,23 @@ QArgs args_of(const qlora_f8& q, const void* x) {
 }  // namespace
 
 qlora_status launch_f8_quantize(const void* X, int32_t x_dtype, const qlora_f8& q,
-                                cudaStream_t s, bool beside_last) {
+                                cudaStream_t s) {
   const QArgs p = args_of(q, X);
   const bool tiles = q.layout == QLORA_F8_TILES, e5 = q.format == QLORA_E5M2;
   if (x_dtype == QLORA_BF16) {
     const bool vec = q.cols % 8 == 0;
     if (vec)
-      return e5 ? quantize_as<__nv_bfloat16, true, true>(p, tiles, beside_last, s)
-                : quantize_as<__nv_bfloat16, false, true>(p, tiles, beside_last, s);
-    return e5 ? quantize_as<__nv_bfloat16, true, false>(p, tiles, beside_last, s)
-              : quantize_as<__nv_bfloat16, false, false>(p, tiles, beside_last, s);
+      return e5 ? quantize_as<__nv_bfloat16, true, true>(p, tiles, s)
+                : quantize_as<__nv_bfloat16, false, true>(p, tiles, s);
+    return e5 ? quantize_as<__nv_bfloat16, true, false>(p, tiles, s)
+              : quantize_as<__nv_bfloat16, false, false>(p, tiles, s);
   }
   const bool vec = q.cols % 4 == 0;
   if (vec)
-    return e5 ? quantize_as<float, true, true>(p, tiles, beside_last, s)
-              : quantize_as<float, false, true>(p, tiles, beside_last, s);
-  return e5 ? quantize_as<float, true, false>(p, tiles, beside_last, s)
-            : quantize_as<float, false, false>(p, tiles, beside_last, s);
+    return e5 ? quantize_as<float, true, true>(p, tiles, s)
+              : quantize_as<float, false, true>(p, tiles, s);
+  return e5 ? quantize_as<float, true, false>(p, tiles, s)
+            : quantize_as<float, false, false>(p, tiles, s);
 }
 
 qlora_status launch_f8_dequantize(const qlora_f8& q, void* out, int32_t out_dtype,

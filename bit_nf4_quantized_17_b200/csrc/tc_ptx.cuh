@@ -130,6 +130,10 @@ __device__ __forceinline__ void bulk_wait_read() {
 }
 
 // ---------------------------------------------------------------- fences
+// Wait until every bulk store of this thread is done, its writes included.
+__device__ __forceinline__ void bulk_wait_all() {
+  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }

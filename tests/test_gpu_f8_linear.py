@@ -302,10 +302,10 @@ def test_gradients_against_differences():
         assert np.abs(_f(got) - want).max() <= tol * np.abs(want).max()
 
 
-@pytest.mark.parametrize("M,launches,lora", [(300, 9, 4), (200, 7, 2)])
-def test_timed_and_counted(M, launches, lora):
+@pytest.mark.parametrize("M", [300, 200])
+def test_timed_and_counted(M):
     """With kernel timing on (event records between the launches) the results are the same.
-    For few tokens one launch quantises and multiplies by the adapter."""
+    One launch quantises and multiplies by the adapter: 2 + 5 in all."""
     N, K, r = 256, 512, 16
     W, A, B, X, dY = (t.to(DEV) for t in _rand_case(M, N, K, r, 12))
     w8 = Q.qlora_f8_quantize(W, Q.QLORA_F8_TILES)
@@ -319,8 +319,8 @@ def test_timed_and_counted(M, launches, lora):
     Q.qlora_timing_begin([Q.QLORA_KERNEL_QUANTIZE, Q.QLORA_KERNEL_LORA_GEMM])
     got = step()
     t = Q.qlora_timing_end()
-    assert Q.qlora_launch_count() - n0 == launches
-    assert t[Q.QLORA_KERNEL_QUANTIZE][1] == 2 and t[Q.QLORA_KERNEL_LORA_GEMM][1] == lora
+    assert Q.qlora_launch_count() - n0 == 7
+    assert t[Q.QLORA_KERNEL_QUANTIZE][1] == 2 and t[Q.QLORA_KERNEL_LORA_GEMM][1] == 2
     for a, b in zip(got, want):
         assert torch.equal(a, b)
 
@@ -355,10 +355,11 @@ def test_workspace_holds_anything(M, N, K, r):
 @pytest.mark.parametrize("M,K,r", [(m, k, r) for m in (1, 5, 8, 9, 16) for k, r in (
     (8, 8), (136, 16), (1096, 40), (4096, 16), (11008, 64), (20000, 256))]
     + [(17, 8, 8), (33, 1096, 40), (100, 4096, 16), (250, 4096, 64), (256, 264, 256),
-       (129, 2048, 136), (257, 128, 8), (40, 20000, 256)])
+       (129, 2048, 136), (257, 128, 8), (40, 20000, 256), (300, 1096, 40), (520, 8, 8),
+       (385, 11008, 64), (1000, 4096, 256), (2050, 520, 104)])
 @pytest.mark.parametrize("fmt,pow2", [(Q.QLORA_E4M3, False), (Q.QLORA_E5M2, True)])
-def test_few_tokens(M, K, r, fmt, pow2):
-    """Up to some hundred tokens: the codes and scales of X that qlora_f8_quantize gives, U against fp64
+def test_codes_and_factor(M, K, r, fmt, pow2):
+    """What the forward makes of X: the codes and scales of X that qlora_f8_quantize gives, U against fp64
     (sums of K terms: K e |x||A|^T), rows past the last token left as they were."""
     W, A, B, X, _ = _rand_case(M, 64, K, r, M + K + r)
     if K > 8:
