@@ -2,8 +2,10 @@
 // f8_quantize.cu) and the LoRA factor U = X A^T (or V = dY B) from one read of X.
 //
 // A CTA takes 128 tokens and a share of the contraction: X and the factor's operand come
-// by TMA in 64-column tiles (128-byte swizzle).  One thread multiplies them into one TMEM
-// accumulator (tcgen05.mma, N = the rank rounded up); beside it two groups of four warps
+// by TMA in 64-column tiles (128-byte swizzle).  One thread multiplies them into four TMEM
+// accumulators in turn (two above rank 128; tcgen05.mma, N = the rank rounded up): sums
+// there are cut off, not rounded, and shorter chains lose less (U of 2048 x 8192 at rank 64
+// against fp64: 3.2e-7, 1.4e-6 in one accumulator; 0.3 us).  Beside it two groups of four warps
 // take the 128-column blocks in turn, a thread a row: the block's 64 words of X in
 // registers give its scale and codes, which leave through shared memory and TMA stores.
 // The shares are summed in distributed shared memory in order, as in gemm_rank.cu.
@@ -37,7 +39,8 @@ constexpr long long kTimeoutCycles = 4000000000ll;
 struct WideArgs {
   int32_t m, kt_total, k_tiles;  // tokens; 64-column tiles, tiles per split (even)
   int32_t b_mn, bn;              // operand of the factor MN-major; MMA N
-  int32_t b_bytes, stage_bytes, stages, tmem_cols, red_ld, area;
+  int32_t b_bytes, stage_bytes, stages, red_ld, area;
+  int32_t accs, acc_cols;        // accumulators, TMEM columns of one (powers of two)
   float* scales;                 // [kb][m]
   int32_t pow2, r, span;
   float* u;                      // m x r or NULL
@@ -134,7 +137,7 @@ f8_front_wide_kernel(const __grid_constant__ CUtensorMap tmX,
     ptx::prefetch_tmap(&tmC);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(tmem_slot, p.tmem_cols);
+    ptx::tmem_alloc(tmem_slot, p.accs * p.acc_cols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -182,10 +185,11 @@ f8_front_wide_kernel(const __grid_constant__ CUtensorMap tmX,
       if (!ptx::mbar_wait(&full[s], ph, kTimeoutCycles, abort_flag)) break;
       ptx::tc_fence_after();
       const uint64_t xd = x0 + off, bd = b0 + off;
-      ptx::umma_bf16(tmem, xd, bd, idesc, i != 0 ? 1u : 0u);
-      ptx::umma_bf16(tmem, xd + (32 >> 4), bd + bs, idesc, 1u);
-      ptx::umma_bf16(tmem, xd + 2 * (32 >> 4), bd + 2 * bs, idesc, 1u);
-      ptx::umma_bf16(tmem, xd + 3 * (32 >> 4), bd + 3 * bs, idesc, 1u);
+      const uint32_t d = tmem + (i & (p.accs - 1)) * p.acc_cols;
+      ptx::umma_bf16(d, xd, bd, idesc, i >= p.accs ? 1u : 0u);
+      ptx::umma_bf16(d, xd + (32 >> 4), bd + bs, idesc, 1u);
+      ptx::umma_bf16(d, xd + 2 * (32 >> 4), bd + 2 * bs, idesc, 1u);
+      ptx::umma_bf16(d, xd + 3 * (32 >> 4), bd + 3 * bs, idesc, 1u);
       ptx::umma_commit(&empty[s]);
       off += p.stage_bytes >> 4;
       if (++s == p.stages) {
@@ -259,18 +263,21 @@ f8_front_wide_kernel(const __grid_constant__ CUtensorMap tmX,
     ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     if (ok) ptx::tc_fence_after();
     for (int c = group; c < p.bn / 16; c += 2) {
-      uint32_t r[16];
-      if (ok) {
-        ptx::tmem_ld_x16(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 16 * c, r);
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+      for (int a = 0; ok && a < min(p.accs, kn); ++a) {
+        uint32_t r[16];
+        ptx::tmem_ld_x16(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + a * p.acc_cols +
+                             16 * c, r);
         ptx::tmem_ld_wait(r);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
       }
       float* dst = red + static_cast<size_t>(row) * p.red_ld + 16 * c;
 #pragma unroll
       for (int j = 0; j < 16; j += 4)
-        *reinterpret_cast<float4*>(dst + j) =
-            ok ? make_float4(__uint_as_float(r[j]), __uint_as_float(r[j + 1]),
-                             __uint_as_float(r[j + 2]), __uint_as_float(r[j + 3]))
-               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        *reinterpret_cast<float4*>(dst + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
     }
   }
   ptx::tc_fence_before();
@@ -338,7 +345,7 @@ f8_front_wide_kernel(const __grid_constant__ CUtensorMap tmX,
   ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, p.tmem_cols);
+    ptx::tmem_dealloc(tmem, p.accs * p.acc_cols);
   }
   if (threadIdx.x == 0 && *abort_flag) report(p.st, QLORA_ERR_DEVICE_TIMEOUT, 140u);
 }
@@ -362,8 +369,9 @@ qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* s
   // a multiple of 4, so that a stage's tiles all go to the same group: it has seen every
   // phase of the barriers that it waits on
   p.stages = kMaxStages * p.stage_bytes <= kStageBudget ? kMaxStages : 4;
-  p.tmem_cols = 32;
-  while (p.tmem_cols < p.bn) p.tmem_cols *= 2;
+  p.acc_cols = 32;
+  while (p.acc_cols < p.bn) p.acc_cols *= 2;
+  p.accs = p.acc_cols > 128 ? 2 : 4;
   p.red_ld = p.bn + 4;
   p.area = static_cast<int32_t>(
       ceil_div(std::max(p.stages * p.stage_bytes, 128 * p.red_ld * 4), 1024) * 1024);
