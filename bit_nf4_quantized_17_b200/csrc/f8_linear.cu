@@ -61,12 +61,10 @@ qlora_status f8_linear_forward(const qlora_f8& W, const void* A, const void* B, 
   const int64_t M = x8.rows, N = W.rows, K = W.cols;
   const Layout L = layout(M, N, r);
   const float sc = lora_scale(alpha, r);
-  const int32_t r16 = lora_rows(r), span = lora_span(r);
   char* ws = static_cast<char*>(workspace);
   auto* st = reinterpret_cast<DeviceStatus*>(ws);
   char* su = ws + L.su;
-  // U = X A^T -> U_save (fp32) and sU = s U as bf16 hi + lo
-  // and the 8 bits of X
+  // U = X A^T -> U_save (fp32) and sU = s U as bf16 hi + lo; the 8 bits of X
   const FrontOp f{X, A, r, false, true, U_save, sc, su, nullptr, 0, 0};
   QLORA_TRY(f8_front_takes(M, K, r) ? f8_front(f, x8, s) : f8_front_wide(f, x8, st, s));
   // starts beside what is ahead of it in this call and reads W at once
