@@ -38,7 +38,7 @@ struct FrontOp {
 };
 bool f8_front_takes(int64_t M, int64_t K, int32_t r);
 qlora_status f8_front(const FrontOp& f, const qlora_f8& x8, cudaStream_t s);
-// f8_front_wide.cu: the same for many tokens; encode has to be set.
+// f8_front_wide.cu: the same for many tokens.
 qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* st,
                            cudaStream_t s);
 

@@ -41,6 +41,7 @@ struct WideArgs {
   int32_t b_mn, bn;              // operand of the factor MN-major; MMA N
   int32_t b_bytes, stage_bytes, stages, red_ld, area;
   int32_t accs, acc_cols;        // accumulators, TMEM columns of one (powers of two)
+  int32_t encode;                // 0: U alone
   float* scales;                 // [kb][m]
   int32_t pow2, r, span;
   float* u;                      // m x r or NULL
@@ -127,7 +128,7 @@ f8_front_wide_kernel(const __grid_constant__ CUtensorMap tmX,
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
       ptx::mbar_init(&full[s], 1);
-      ptx::mbar_init(&empty[s], 5);  // the MMAs, and four warps that encode
+      ptx::mbar_init(&empty[s], p.encode ? 5 : 1);  // the MMAs, and four warps that encode
     }
     ptx::mbar_init(accum, 1);
     *abort_flag = 0;
@@ -228,7 +229,7 @@ f8_front_wide_kernel(const __grid_constant__ CUtensorMap tmX,
       step();
       step();
     }
-    for (int i = 2 * group; i < kn; i += 4) {
+    for (int i = 2 * group; p.encode && i < kn; i += 4) {
       uint32_t w0[32], w1[32];
       take(w0);
       float a = amax_words<__nv_bfloat16>(w0);
@@ -347,7 +348,7 @@ f8_front_wide_kernel(const __grid_constant__ CUtensorMap tmX,
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, p.accs * p.acc_cols);
   }
-  if (threadIdx.x == 0 && *abort_flag) report(p.st, QLORA_ERR_DEVICE_TIMEOUT, 140u);
+  if (threadIdx.x == 0 && *abort_flag) report(p.st, QLORA_ERR_DEVICE_TIMEOUT, 150u);
 }
 
 }  // namespace
@@ -355,7 +356,7 @@ f8_front_wide_kernel(const __grid_constant__ CUtensorMap tmX,
 qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* st,
                            cudaStream_t s) {
   const int64_t M = x8.rows, K = x8.cols;
-  if (M < 1 || K % 8 != 0 || f.r % 8 != 0 || f.r > 256 || !f.encode) return QLORA_ERR_UNSUPPORTED;
+  if (M < 1 || K % 8 != 0 || f.r % 8 != 0 || f.r > 256) return QLORA_ERR_UNSUPPORTED;
   const int64_t m_tiles = ceil_div(M, 128);
   if (m_tiles > 65535) return QLORA_ERR_SHAPE;
   WideArgs p{};
@@ -375,6 +376,7 @@ qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* s
   p.red_ld = p.bn + 4;
   p.area = static_cast<int32_t>(
       ceil_div(std::max(p.stages * p.stage_bytes, 128 * p.red_ld * 4), 1024) * 1024);
+  p.encode = f.encode ? 1 : 0;
   p.scales = x8.scales;
   p.pow2 = x8.pow2;
   p.r = f.r;
@@ -386,12 +388,13 @@ qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* s
   p.ut_lo = f.ut_lo;
   p.st = st;
   CUtensorMap mx, mb, mc;
-  const bool ok =
-      make_map(&mx, f.x, true, K, M, K, 64, 128, true) &&
-      (f.along ? make_map(&mb, f.a, true, f.r, K, f.r, 64, 64, true)
-               : make_map(&mb, f.a, true, K, f.r, K, 64, static_cast<uint32_t>(p.bn), true)) &&
-      // zeros up to the next multiple of 16 columns
-      make_map(&mc, x8.codes, false, ceil_div(K, 16) * 16, M, x8.ld, 128, 128, true);
+  bool ok = make_map(&mx, f.x, true, K, M, K, 64, 128, true) &&
+            (f.along ? make_map(&mb, f.a, true, f.r, K, f.r, 64, 64, true)
+                     : make_map(&mb, f.a, true, K, f.r, K, 64, static_cast<uint32_t>(p.bn), true));
+  mc = mx;
+  // zeros up to the next multiple of 16 columns
+  if (f.encode)
+    ok = ok && make_map(&mc, x8.codes, false, ceil_div(K, 16) * 16, M, x8.ld, 128, 128, true);
   if (!ok) return QLORA_ERR_CUDA;
   const bool e5 = x8.format == QLORA_E5M2;
   const void* fn = e5 ? reinterpret_cast<const void*>(f8_front_wide_kernel<true>)
@@ -432,9 +435,10 @@ qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* s
   p.k_tiles = 2 * static_cast<int32_t>(ceil_div(kbs, splits));
   void* args[] = {&mx, &mb, &mc, &p};
   count_launch();
-  timing_mark(QLORA_KERNEL_QUANTIZE, s, true);
+  const int kind = f.encode ? QLORA_KERNEL_QUANTIZE : QLORA_KERNEL_LORA_GEMM;
+  timing_mark(kind, s, true);
   const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
-  timing_mark(QLORA_KERNEL_QUANTIZE, s, false);
+  timing_mark(kind, s, false);
   if (e != cudaSuccess) {
     (void)cudaGetLastError();
     return QLORA_ERR_CUDA;

@@ -78,7 +78,7 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
   const int64_t M = x8.rows, N = W.rows, K = W.cols;
   const Layout L = layout(M, N, r);
   const float sc = lora_scale(alpha, r);
-  const int32_t r16 = lora_rows(r), span = lora_span(r);
+  const int32_t r16 = lora_rows(r);
   const int64_t mp = pad8(M);
   char* ws = static_cast<char*>(workspace);
   auto* st = reinterpret_cast<DeviceStatus*>(ws);
@@ -101,19 +101,7 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
   auto v_work = [&]() -> qlora_status {
     const FrontOp f{dY, B, r, true, dX != nullptr, small ? v : nullptr, sc, sv,
                     small ? nullptr : vt, mp, r16};
-    if (f8_front_takes(M, N, r)) return f8_front(f, dy8, s);
-    if (dX) return f8_front_wide(f, dy8, st, s);
-    ReduceArgs ra = reduce_args(nullptr, 1, M, r, r16);
-    ra.o2 = sv;
-    ra.ld2 = 2 * span;
-    ra.a2 = sc;
-    ra.o2_lo = span;
-    ra.o2_pad = 1;
-    ra.o3 = vt;
-    ra.ld3 = mp;
-    ra.a3 = 1.0f;
-    ra.o3_lo = r16;
-    return tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s);
+    return f8_front_takes(M, N, r) ? f8_front(f, dy8, s) : f8_front_wide(f, dy8, st, s);
   };
   auto grad_b = [&]() -> qlora_status {
     if (small) return small_grad_b(dY, U, static_cast<int>(M), N, r, sc, accumulate, dB, s2);

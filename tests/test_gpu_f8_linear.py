@@ -409,7 +409,7 @@ def test_weight_written_just_before(M):
             assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("M", [3, 16, 50, 256])
+@pytest.mark.parametrize("M", [3, 16, 50, 256, 300, 700])
 def test_few_tokens_captured_and_without_dx(M):
     """Captured and replayed on new inputs; dA and dB without dX are those with it."""
     N, K, r = 264, 1096, 24
