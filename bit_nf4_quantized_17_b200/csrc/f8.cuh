@@ -59,6 +59,10 @@ struct F8Lora {
 qlora_status f8_gemm(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,
                      const F8Lora& lora, cudaStream_t s);
 
+// f8_gemm.cu: clusters of such a launch (all CTAs along z) that run at once.  A cluster lies
+// within one group of SMs: of size 8 at one CTA per SM fewer than 16 do.
+int f8_resident_clusters(const void* fn, const cudaLaunchConfig_t& cfg);
+
 // f8_grad.cu: dA (r x d_in fp32) = sc V^T X^ from X kept by rows in 8 bits (added to
 // dA when accumulate).  More than 16 tokens: V^T as bf16 hi rows [0, r) and lo
 // rows from lora_rows(r) on, ld_v elements a row; r a multiple of 8 up to 256.  Up

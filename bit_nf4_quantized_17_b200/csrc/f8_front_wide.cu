@@ -420,17 +420,7 @@ qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* s
   for (;; --splits) {
     attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
     cfg.gridDim = dim3(1u, static_cast<unsigned>(m_tiles), static_cast<unsigned>(splits));
-    if (splits == 1) break;
-    int resident = 0;
-    constexpr int kClusterTag = 16;  // one CTA per SM: the answer does not depend on the rank
-    if (!cached_value(fn, kClusterTag + splits, &resident)) {
-      if (cudaOccupancyMaxActiveClusters(&resident, fn, &cfg) != cudaSuccess) {
-        (void)cudaGetLastError();
-        resident = 0;
-      }
-      store_value(fn, kClusterTag + splits, resident);
-    }
-    if (m_tiles <= resident) break;
+    if (splits == 1 || m_tiles <= f8_resident_clusters(fn, cfg)) break;
   }
   p.k_tiles = 2 * static_cast<int32_t>(ceil_div(kbs, splits));
   void* args[] = {&mx, &mb, &mc, &p};

@@ -466,21 +466,6 @@ int split_count(int64_t tiles, int64_t kb, int64_t slots) {
   return static_cast<int>(std::max<int64_t>(1, s));
 }
 
-// Clusters of `splits` CTAs that run at once, asked for once per kernel, size and
-// device.  (For the kernel of one CTA per SM: a split has at least 4 blocks, so 4 stages,
-// 128 KB, and the answer does not depend on how many more it has.)
-int resident_clusters(const void* fn, const cudaLaunchConfig_t& cfg, int splits) {
-  constexpr int kClusterTag = 16;
-  int n = 0;
-  if (cached_value(fn, kClusterTag + splits, &n)) return n;
-  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
-    (void)cudaGetLastError();
-    n = 0;
-  }
-  store_value(fn, kClusterTag + splits, n);
-  return n;
-}
-
 template <int BN, bool SWAP>
 qlora_status launch(const qlora_f8& a, const qlora_f8& b, bool trans_b, GemmArgs p,
                     const F8Lora& l, cudaStream_t s) {
@@ -540,7 +525,7 @@ qlora_status launch(const qlora_f8& a, const qlora_f8& b, bool trans_b, GemmArgs
     // run at once: 256 x 1024 x 4096, 16 tiles, took 14.2 us in 8 splits and takes 7.9 in
     // as many as do.  Two CTAs per SM read for one another while some wait: 16 x 11008 x
     // 4096, 86 tiles, 7.8 us in 3 splits, 10.3 in the 2 that would all be resident.
-    if (C::kPerSm == 2 || splits == 1 || tiles <= resident_clusters(fn, cfg, splits)) break;
+    if (C::kPerSm == 2 || splits == 1 || tiles <= f8_resident_clusters(fn, cfg)) break;
   }
   count_launch();
   const cudaError_t e = cudaLaunchKernelEx(&cfg, f8_gemm_kernel<BN, SWAP>, SWAP ? mb : ma,
@@ -601,6 +586,20 @@ qlora_status f8_gemm(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c
     if (two < one) return f8_gemm_pairs(a, b, trans_b, c, c_f32, l, s);
   }
   return launch<128, false>(a, b, trans_b, p, l, s);
+}
+
+int f8_resident_clusters(const void* fn, const cudaLaunchConfig_t& cfg) {
+  // one answer per kernel, device, cluster size and KB of shared memory
+  const int tag = 16 + static_cast<int>(cfg.gridDim.z) +
+                  256 * static_cast<int>(cfg.dynamicSmemBytes >> 10);
+  int n = 0;
+  if (cached_value(fn, tag, &n)) return n;
+  if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+    (void)cudaGetLastError();
+    n = 0;
+  }
+  store_value(fn, tag, n);
+  return n;
 }
 
 int f8::sm_count() {

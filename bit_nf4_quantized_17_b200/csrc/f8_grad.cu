@@ -365,17 +365,14 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
   const qlora_status cs = ensure_smem(reinterpret_cast<const void*>(fn), 200 * 1024);
   if (cs != QLORA_OK) return cs;
   const int64_t tiles = ceil_div(K, 128);
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    (void)cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  // splits of the tokens: as many CTAs as run at once (two per SM where the
-  // shared memory allows), at least 4 tiles each
-  const int64_t slots = (smem <= 112 * 1024 ? 2 : 1) * sms;
-  const int64_t want = std::min<int64_t>({8, slots / (tiles * chunks), p.kt_total / 4});
-  const int splits = static_cast<int>(std::max<int64_t>(1, want));
-  p.kt_per = static_cast<int32_t>(ceil_div(p.kt_total, splits));
+  // Splits of the tokens, at least 4 tiles each: whichever ends soonest, rounds of clusters
+  // that run at once times the tiles of one and about four for its start and sum.
+  // (Backward without dX against as many CTAs as the SMs hold: 4096 tokens x 2048 at rank
+  // 128 62.2 us, was 74.8; 2048 x 4096 at rank 64 28.4, 31.5; 8192 x 4096 at rank 16 34.8,
+  // 33.0.)
+  const int64_t want = std::min<int64_t>(8, p.kt_total / 4);
+  int splits = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles), chunks, splits);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -383,9 +380,22 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1;
   attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  const void* kernel = reinterpret_cast<const void*>(fn);
+  int64_t least = 0;
+  for (int n = static_cast<int>(std::max<int64_t>(1, want)); n >= 1; --n) {
+    attr[0].val.clusterDim.z = static_cast<unsigned>(n);
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles), chunks, n);
+    const int64_t at_once = std::max(1, f8_resident_clusters(kernel, cfg));
+    const int64_t cost = ceil_div(tiles * chunks, at_once) * (ceil_div(p.kt_total, n) + 4);
+    if (least != 0 && cost >= least) continue;
+    least = cost;
+    splits = n;
+  }
+  attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles), chunks, splits);
+  p.kt_per = static_cast<int32_t>(ceil_div(p.kt_total, splits));
   count_launch();
   timing_mark(QLORA_KERNEL_LORA_GEMM, s, true);
   const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, mx, mv, p);
