@@ -2,6 +2,7 @@
 #pragma once
 
 #include "f8.cuh"
+#include "f8_ring.cuh"
 #include "tc_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -28,17 +29,9 @@ struct GemmArgs {
   uint32_t idesc, idesc_ext;
 };
 
-// Scales on their way to the epilogue warps: a ring of two chunks of kChunk
-// blocks in shared memory, filled by one warp with 4-byte asynchronous copies
-// (any alignment), so that no epilogue warp waits for global memory and a block's
-// scales are two or three shared-memory loads, issued a block ahead.
-constexpr int kChunk = 16;
-template <int ROWS, int COLS>  // A's scales of ROWS rows, B's of COLS block columns
-struct ScaleRing {
-  float a[2][kChunk][ROWS];
-  float b[2][kChunk][COLS];
-};
-
+// The scale ring (f8_ring.cuh) is filled by one warp with 4-byte asynchronous copies (any
+// alignment), so that no epilogue warp waits for global memory and a block's scales are two
+// or three shared-memory loads, issued a block ahead.
 static __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(ptx::smem_u32(dst)), "l"(src)
                : "memory");
@@ -55,10 +48,11 @@ static __device__ __forceinline__ void cp_async_wait_all() {
 // Fills one chunk: blocks [kb, kb + kChunk) below kb_end, A's rows from `row`, B's
 // scale columns from `col` (of `cols`).  Rows and columns past the end repeat the
 // last one: what they scale is not stored.  All lanes of one warp; `full` counts 32.
-template <int ROWS, int COLS>
-static __device__ __forceinline__ void fill_scales(const GemmArgs& p, ScaleRing<ROWS, COLS>* ring,
-                                                   int slot, int kb, int kb_end, int row, int col,
-                                                   int cols, int lane, uint64_t* full) {
+template <int ROWS, int COLS, int SPARE>
+static __device__ __forceinline__ void fill_scales(const GemmArgs& p,
+                                                   ScaleRing<ROWS, COLS, SPARE>* ring, int slot,
+                                                   int kb, int kb_end, int row, int col, int cols,
+                                                   int lane, uint64_t* full) {
   const int n = min(kChunk, kb_end - kb);
   for (int i = 0; i < n; ++i) {
     const float* sa = p.sa + static_cast<int64_t>(kb + i) * p.m;

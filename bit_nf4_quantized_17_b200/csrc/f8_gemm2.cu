@@ -51,7 +51,7 @@ constexpr int kRoleRegs = 40, kSumRegs = 232;  // registers a thread, from 168 a
 constexpr int kStages = 5;
 constexpr int kOpBytes = 16384;              // 128 rows x 128 bytes: A, and this CTA's half of B
 constexpr int kStageBytes = 2 * kOpBytes;
-using Ring = f8::ScaleRing<128, 2>;
+using Ring = f8::PairRing;
 constexpr int kOutBytes = 4096;              // a warp's part of C on its way: 32 rows x 128 bytes
 constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpi * kOutBytes + sizeof(Ring) + 256;
 constexpr int kGroup = 16;                   // row tiles per column tile before the next one
@@ -338,17 +338,17 @@ f8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         ok = ptx::mbar_wait(&sc_full[chunk & 1], (chunk >> 1) & 1, kTimeoutCycles, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        uint32_t pa = sa_base + (chunk & 1) * (f8::kChunk * 512);
-        uint32_t pb = sb_base + (chunk & 1) * (f8::kChunk * 8);
+        uint32_t pa = sa_base + Ring::a_at(chunk, 0);
+        uint32_t pb = sb_base + Ring::b_at(chunk, 0);
         float sa = ptx::lds_f32(pa);
         float2 sb = ptx::lds_f32x2(pb);
         const int n = min(f8::kChunk, kn - k0);
         for (int i = 0; i < n && ok; ++i) {
           const float s0 = sa * sb.x, s1 = sa * sb.y;
-          // the next block's scales, on their way while this one is added (the
-          // last read of a chunk runs past it, inside the ring, and is not used)
-          pa += 512;
-          pb += 8;
+          // the next block's scales, on their way while this one is added (past the
+          // last block of a chunk: the ring's spare row, not used)
+          pa += Ring::a_at(0, 1);
+          pb += Ring::b_at(0, 1);
           add_block(s0, s1, [&]() {
             sa = ptx::lds_f32(pa);
             sb = ptx::lds_f32x2(pb);
