@@ -62,7 +62,21 @@ __device__ __forceinline__ void tile_at(const GemmArgs& p, int m_tiles, int t, i
   *mt = g * kTileGroup + in - *nt * rows;
 }
 
-__device__ __forceinline__ uint32_t exponent(float s) { return (__float_as_uint(s) >> 23) & 0xffu; }
+// A scale's bits.  The launch ahead may write the scales while this one is already resident,
+// so they are not read-only for this kernel's life: a plain load, not one through the
+// read-only path, and volatile, so that it stays behind the dependency wait.
+__device__ __forceinline__ uint32_t scale_bits(const float* s) {
+  uint32_t u;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(u) : "l"(s));
+  return u;
+}
+// Four scales' exponents as the bytes of a word.
+__device__ __forceinline__ uint32_t exponents(const uint32_t (&u)[4]) {
+  uint32_t w = 0u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w |= ((u[j] >> 23) & 0xffu) << (8 * j);
+  return w;
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
 f8_pow2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -260,26 +274,26 @@ f8_pow2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       for (int k0 = 0; k0 < kn; k0 += 4) {
         // rows and columns past the end repeat the last one: their products are not stored;
         // blocks past the end are not multiplied
+        // (all loads before the first use); a tile's 192 columns lie in two column blocks of
+        // B, from 0 or 64 into the first
+        uint32_t ra[4][4], rb[2][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int64_t kb = min(k0 + j, kn - 1);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            ra[c][j] = scale_bits(p.sa + kb * p.m + min(row0 + 32 * c, p.m - 1));
+#pragma unroll
+          for (int b = 0; b < 2; ++b)
+            rb[b][j] = scale_bits(p.sb + min(((nt * kBN) >> 7) + b, nbs - 1) * p.sb_n + kb * p.sb_k);
+        }
         uint32_t wa[4], wb[8];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          wa[c] = 0u;
+        for (int c = 0; c < 4; ++c) wa[c] = exponents(ra[c]);
+        const uint32_t first = exponents(rb[0]), second = exponents(rb[1]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int64_t kb = min(k0 + j, kn - 1);
-            wa[c] |= exponent(__ldg(p.sa + kb * p.m + min(row0 + 32 * c, p.m - 1))) << (8 * j);
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          wb[c] = 0u;
-          const int nb = min((nt * kBN + 32 * min(c, 5)) >> 7, nbs - 1);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int64_t kb = min(k0 + j, kn - 1);
-            wb[c] |= exponent(__ldg(p.sb + nb * p.sb_n + kb * p.sb_k)) << (8 * j);
-          }
-        }
+        for (int c = 0; c < 8; ++c)
+          wb[c] = ((nt * kBN) & 127) + 32 * min(c, 5) < 128 ? first : second;
         ok = ptx::mbar_wait(&exp_empty[g], ph, kTimeoutCycles, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
