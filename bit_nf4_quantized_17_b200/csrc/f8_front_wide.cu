@@ -8,7 +8,9 @@
 // against fp64: 3.2e-7, 1.4e-6 in one accumulator; 0.3 us).  Beside it two groups of four warps
 // take the 128-column blocks in turn, a thread a row: the block's 64 words of X in
 // registers give its scale and codes, which leave through shared memory and TMA stores.
-// The shares are summed in distributed shared memory in order, as in gemm_rank.cu.
+// The shares are summed in distributed shared memory in order, as in gemm_rank.cu.  Every wait
+// is bounded; one that gives up reports QLORA_ERR_DEVICE_TIMEOUT and leaves NaN in the factor
+// of its tokens.
 //
 // Bound by latency within a block (load, maximum, encoding, store, two groups deep) and
 // by the sum across the cluster: 19 us alone and cold for 2048 x 8192 at rank 64, 8 of
@@ -283,6 +285,10 @@ f8_front_wide_kernel(const __grid_constant__ CUtensorMap tmX,
   }
   ptx::tc_fence_before();
   __syncthreads();
+  // a wait of this CTA gave up: its sums are not whole (the status word may not be read)
+  if (*abort_flag)
+    for (int e = threadIdx.x; e < 128 * p.red_ld; e += kThreads)
+      red[e] = __int_as_float(0x7fffffff);
   ptx::cluster_sync();
 
   // --------------------------- sum over the splits, in order, and store

@@ -15,7 +15,7 @@
 // threads): warp 0 loads codes, warp 2 loads V^T, warp 1 owns TMEM and issues
 // the MMAs, warps 4-11 expand in two groups (group g takes 64-token tiles
 // i % 2 == g), warps 4-7 drain.  Every wait is bounded; a wait that gives up
-// reports QLORA_ERR_DEVICE_TIMEOUT.
+// reports QLORA_ERR_DEVICE_TIMEOUT and leaves NaN in its columns of dA.
 // Up to 16 tokens: CUDA cores, bound by writing dA; a thread takes 16 columns of 4
 // ranks, so that each code is expanded once for 4 ranks.
 #include <cudaTypedefs.h>
@@ -225,6 +225,10 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   }
   ptx::tc_fence_before();
   __syncthreads();
+  // a wait of this CTA gave up: its sums are not whole (the status word may not be read)
+  if (*abort_flag)
+    for (int e = threadIdx.x; e < 2 * p.rc * kRedLd; e += kThreads)
+      red[e] = __int_as_float(0x7fffffff);
   ptx::cluster_sync();
   // ---------------------------------------- hi + lo over the splits, in order
   const int cols = min(p.rc, p.r - j0);
