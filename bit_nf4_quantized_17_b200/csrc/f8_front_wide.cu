@@ -123,7 +123,7 @@ f8_front_wide_kernel(const __grid_constant__ CUtensorMap tmX,
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t S = gridDim.z, z = blockIdx.z;  // the cluster spans z
-  const int m0 = blockIdx.y * 128;
+  const int m0 = blockIdx.x * 128;
   const int kt0 = static_cast<int>(z) * p.k_tiles;
   const int kn = max(0, min(p.k_tiles, p.kt_total - kt0));
 
@@ -364,7 +364,6 @@ qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* s
   const int64_t M = x8.rows, K = x8.cols;
   if (M < 1 || K % 8 != 0 || f.r % 8 != 0 || f.r > 256) return QLORA_ERR_UNSUPPORTED;
   const int64_t m_tiles = ceil_div(M, 128);
-  if (m_tiles > 65535) return QLORA_ERR_SHAPE;
   WideArgs p{};
   p.m = static_cast<int32_t>(M);
   p.kt_total = static_cast<int32_t>(ceil_div(K, 64));
@@ -425,7 +424,7 @@ qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* s
   int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, sms / m_tiles, kbs / 4})));
   for (;; --splits) {
     attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
-    cfg.gridDim = dim3(1u, static_cast<unsigned>(m_tiles), static_cast<unsigned>(splits));
+    cfg.gridDim = dim3(static_cast<unsigned>(m_tiles), 1u, static_cast<unsigned>(splits));
     if (splits == 1 || m_tiles <= f8_resident_clusters(fn, cfg)) break;
   }
   p.k_tiles = 2 * static_cast<int32_t>(ceil_div(kbs, splits));

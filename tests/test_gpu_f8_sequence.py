@@ -36,3 +36,21 @@ def test_scales_written_just_before(m, n, k, trans, pow2):
     got = [(i % 3, step(i % 3, False)) for i in range(12)]
     for i, c in got:
         assert torch.equal(c, want[i])
+
+
+def test_more_row_tiles_than_a_grid_has_rows():
+    """More than 65535 tiles of 128 tokens: the last rows are those of the same tokens alone."""
+    M, N, K, r, tail = 65535 * 128 + 333, 8, 16, 8, 300
+    bf16 = torch.bfloat16
+    A, B = (_randn(1, r, K) / 3).to(bf16), _randn(2, N, r).to(bf16)
+    X, dY = _randn(3, M, K).to(bf16), _randn(4, M, N).to(bf16)
+    w8 = Q.qlora_f8_quantize(_randn(5, N, K), Q.QLORA_F8_TILES)
+
+    def run(x, dy):
+        m = x.shape[0]
+        x8, U = Q.F8Matrix.empty(m, K), torch.empty((m, r), device=DEV)
+        Y = Q.qlora_f8_linear_fwd(w8, A, B, 16.0, x, x8, U_save=U, check=True)
+        dX, _, _ = Q.qlora_f8_linear_bwd(w8, A, B, 16.0, x8, U, dy, check=True)
+        return Y, U, x8.codes, x8.scales.t(), dX
+    for got, alone in zip(run(X, dY), run(X[-tail:].contiguous(), dY[-tail:].contiguous())):
+        assert torch.equal(got[-tail:], alone)
