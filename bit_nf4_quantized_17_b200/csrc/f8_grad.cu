@@ -11,7 +11,12 @@
 // More than 16 tokens: D = X^T V^T per 128 columns of X on the tensor cores
 // (tcgen05.mma kind::f16, M = 128, N = 2 rc), V in bf16 as hi + lo (accurate to about
 // 2^-17; rank chunks of rc <= 128), the contraction split over a cluster and
-// summed in distributed shared memory in split order, as in gemm_rank.cu.  Roles (384
+// summed in distributed shared memory in split order, as in gemm_rank.cu.  Sums in TMEM are
+// cut off, not rounded, which adds up along a chain of MMAs: a split takes its tiles in
+// turn into as many accumulators as keep the chains at 32 MMAs (512 tokens), as far as
+// TMEM goes, and tokens past 64 MMAs a chain are a launch of their own that adds to dA.
+// Relative to fp64 at rank 16, 4096 columns: 4096 tokens 2.55e-6, 65536 3.1e-6 (2.7e-6 and
+// 2.0e-5 in one accumulator and launch); 2.5e-6 of it are V's two terms.  Roles (384
 // threads): warp 0 loads codes, warp 2 loads V^T, warp 1 owns TMEM and issues
 // the MMAs, warps 4-11 expand in two groups (group g takes 64-token tiles
 // i % 2 == g), warps 4-7 drain.  Every wait is bounded; a wait that gives up
@@ -23,6 +28,7 @@
 #include <algorithm>
 
 #include "f8.cuh"
+#include "linear.cuh"
 #include "tc_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -34,15 +40,18 @@ constexpr int kABytes = 16384;     // 64 tokens x 128 columns in bf16, two 64-co
 constexpr int kCodeBytes = 8192;   // 64 tokens x 128 codes
 constexpr int kCodeSlots = 4;
 constexpr int kStages = 2;
+constexpr int kChain = 32, kMaxChain = 64;  // MMAs into one accumulator: wanted, at most
+constexpr int kMaxSmem = 227 * 1024;
+constexpr int kSmemPerColumn = 228 * 1024 / 512;  // of an SM's shared memory to its TMEM columns
 constexpr long long kTimeoutCycles = 4000000000ll;
 
 struct GradArgs {
   const float* scales;   // [kb][m]
   int32_t m, k;          // tokens, columns of X
-  int32_t kt_total, kt_per;  // 64-token tiles, tiles per split
+  int32_t kt0, kt_end, kt_per;  // 64-token tiles of this launch, tiles per split
   int32_t r, rc, lo_row;     // rank, ranks per chunk (a multiple of 16), first lo row of V^T
   int32_t area;          // bytes of the tiles (the partial sums reuse them)
-  int32_t tmem_cols;
+  int32_t accs, acc_cols;    // accumulators, TMEM columns of one (powers of two)
   float* dA;
   float sc;
   int32_t accumulate;
@@ -87,8 +96,8 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   const uint32_t S = gridDim.z, z = blockIdx.z;
   const int kb = blockIdx.x, k0 = kb * 128;
   const int j0 = blockIdx.y * p.rc;  // first rank of the chunk
-  const int t0 = static_cast<int>(z) * p.kt_per;
-  const int tn = max(0, min(p.kt_per, p.kt_total - t0));
+  const int t0 = p.kt0 + static_cast<int>(z) * p.kt_per;
+  const int tn = max(0, min(p.kt_per, p.kt_end - t0));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kCodeSlots; ++s) {
@@ -107,7 +116,7 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     ptx::prefetch_tmap(&tmV);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(tmem_slot, p.tmem_cols);
+    ptx::tmem_alloc(tmem_slot, p.accs * p.acc_cols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -156,10 +165,11 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
       // A: MN-major, two 64-column halves 8192 bytes apart, 16 tokens (2048 bytes) a step
       const uint64_t ad = ptx::sw128_desc(a_addr, 8192, 1024);
       const uint64_t bd = ptx::sw128_desc(a_addr + kABytes, 16, 1024);
+      const uint32_t d = tmem + (i & (p.accs - 1)) * p.acc_cols;
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        ptx::umma_bf16(tmem, ad + ((2048 * ks) >> 4), bd + ((32 * ks) >> 4), p.idesc,
-                       (i | ks) != 0 ? 1u : 0u);
+        ptx::umma_bf16(d, ad + ((2048 * ks) >> 4), bd + ((32 * ks) >> 4), p.idesc,
+                       i >= p.accs || ks != 0 ? 1u : 0u);
       ptx::umma_commit(&empty[s]);
     }
     ptx::umma_commit(accum);
@@ -213,14 +223,19 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     if (ok) ptx::tc_fence_after();
     for (int c = 0; c < 2 * p.rc; c += 16) {
-      uint32_t r[16];
-      if (ok) {
-        ptx::tmem_ld_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, r);
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = 0.0f;
+      for (int a = 0; ok && a < min(p.accs, tn); ++a) {
+        uint32_t r[16];
+        ptx::tmem_ld_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + a * p.acc_cols + c,
+                         r);
         ptx::tmem_ld_wait(r);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
       }
 #pragma unroll
-      for (int j = 0; j < 16; ++j)
-        red[(c + j) * kRedLd + i] = ok ? __uint_as_float(r[j]) : 0.0f;
+      for (int j = 0; j < 16; ++j) red[(c + j) * kRedLd + i] = v[j];
     }
   }
   ptx::tc_fence_before();
@@ -252,7 +267,7 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, p.tmem_cols);
+    ptx::tmem_dealloc(tmem, p.accs * p.acc_cols);
   }
   if (threadIdx.x == 0 && *abort_flag) report(p.st, QLORA_ERR_DEVICE_TIMEOUT, 140u);
 }
@@ -351,34 +366,30 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
   p.scales = x.scales;
   p.m = static_cast<int32_t>(M);
   p.k = static_cast<int32_t>(K);
-  p.kt_total = static_cast<int32_t>(ceil_div(M, 64));
   p.r = r;
   p.lo_row = r16;
   p.area = std::max(kStages * (kABytes + 2 * p.rc * 128) + kCodeSlots * kCodeBytes,
                     2 * p.rc * 132 * 4);
-  p.tmem_cols = 32;
-  while (p.tmem_cols < 2 * p.rc) p.tmem_cols *= 2;
+  p.acc_cols = 32;
+  while (p.acc_cols < 2 * p.rc) p.acc_cols *= 2;
   p.dA = dA;
   p.sc = sc;
-  p.accumulate = accumulate ? 1 : 0;
   p.idesc = ptx::idesc_bf16(128, 2 * p.rc, 1, 0);
   p.st = st;
   const bool e5 = x.format == QLORA_E5M2;
   auto* fn = e5 ? f8_grad_kernel<true> : f8_grad_kernel<false>;
-  const size_t smem = 1024 + static_cast<size_t>(p.area) + 256;
-  const qlora_status cs = ensure_smem(reinterpret_cast<const void*>(fn), 200 * 1024);
+  const void* kernel = reinterpret_cast<const void*>(fn);
+  const qlora_status cs = ensure_smem(kernel, kMaxSmem);
   if (cs != QLORA_OK) return cs;
+  const int need = 1024 + p.area + 256;
+  // TMEM columns of a CTA: half of them where two share an SM.  A CTA asks for at least the
+  // shared memory that goes with its columns, so that no other kernel's CTA that needs TMEM
+  // finds room beside it and has to wait for this one while its cluster waits for it.
+  const int max_accs = (need > kMaxSmem / 2 - 1024 ? 512 : 256) / p.acc_cols;
+  const int64_t kt_total = ceil_div(M, 64);
   const int64_t tiles = ceil_div(K, 128);
-  // Splits of the tokens, at least 4 tiles each: whichever ends soonest, rounds of clusters
-  // that run at once times the tiles of one and about four for its start and sum.
-  // (Backward without dX against as many CTAs as the SMs hold: 4096 tokens x 2048 at rank
-  // 128 62.2 us, was 74.8; 2048 x 4096 at rank 64 28.4, 31.5; 8192 x 4096 at rank 16 34.8,
-  // 33.0.)
-  const int64_t want = std::min<int64_t>(8, p.kt_total / 4);
-  int splits = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -386,29 +397,51 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
   attr[0].val.clusterDim.y = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const void* kernel = reinterpret_cast<const void*>(fn);
-  int64_t least = 0;
-  for (int n = static_cast<int>(std::max<int64_t>(1, want)); n >= 1; --n) {
+  // One launch in n splits over `per` tiles each: its shared memory and grid.
+  auto plan = [&](int n, int64_t per) {
+    p.kt_per = static_cast<int32_t>(per);
+    for (p.accs = 1; p.accs < max_accs && 4 * per > kChain * p.accs;) p.accs *= 2;
+    cfg.dynamicSmemBytes = std::max(need, p.accs * p.acc_cols * kSmemPerColumn - 1024);
     attr[0].val.clusterDim.z = static_cast<unsigned>(n);
     cfg.gridDim = dim3(static_cast<unsigned>(tiles), chunks, n);
+  };
+  // Splits of the tokens, at least 4 tiles each: whichever ends soonest, launches times
+  // rounds of clusters that run at once times the tiles of one and about four for its start
+  // and sum.
+  // (Backward without dX against as many CTAs as the SMs hold: 4096 tokens x 2048 at rank
+  // 128 62.2 us, was 74.8; 2048 x 4096 at rank 64 28.4, 31.5; 8192 x 4096 at rank 16 34.8,
+  // 33.0.)
+  int splits = 1;
+  int64_t least = 0, launches = 1;
+  for (int n = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, kt_total / 4))); n >= 1;
+       --n) {
+    const int64_t times = ceil_div(kt_total, n * (kMaxChain / 4) * max_accs);
+    const int64_t per = ceil_div(ceil_div(kt_total, times), n);
+    plan(n, per);
     const int64_t at_once = std::max(1, f8_resident_clusters(kernel, cfg));
-    const int64_t cost = ceil_div(tiles * chunks, at_once) * (ceil_div(p.kt_total, n) + 4);
+    const int64_t cost = times * ceil_div(tiles * chunks, at_once) * (per + 4);
     if (least != 0 && cost >= least) continue;
     least = cost;
     splits = n;
+    launches = times;
   }
-  attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles), chunks, splits);
-  p.kt_per = static_cast<int32_t>(ceil_div(p.kt_total, splits));
-  count_launch();
-  timing_mark(QLORA_KERNEL_LORA_GEMM, s, true);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, mx, mv, p);
-  timing_mark(QLORA_KERNEL_LORA_GEMM, s, false);
-  if (e != cudaSuccess) {
-    (void)cudaGetLastError();
-    return QLORA_ERR_CUDA;
+  const int64_t each = ceil_div(kt_total, launches);
+  plan(splits, ceil_div(each, splits));
+  for (int64_t kt0 = 0; kt0 < kt_total; kt0 += each) {
+    p.kt0 = static_cast<int32_t>(kt0);
+    p.kt_end = static_cast<int32_t>(std::min(kt_total, kt0 + each));
+    p.accumulate = accumulate || kt0 > 0 ? 1 : 0;
+    count_launch();
+    timing_mark(QLORA_KERNEL_LORA_GEMM, s, true);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fn, mx, mv, p);
+    timing_mark(QLORA_KERNEL_LORA_GEMM, s, false);
+    if (e != cudaSuccess) {
+      (void)cudaGetLastError();
+      return QLORA_ERR_CUDA;
+    }
+    QLORA_TRY(after_launch("f8_grad_a", s));
   }
-  return after_launch("f8_grad_a", s);
+  return QLORA_OK;
 }
 
 }  // namespace qlora

@@ -1,0 +1,62 @@
+"""GPU: how close the fp32 outputs of the 8-bit layers are to fp64 as a whole, in the norm,
+beside the bounds per element of test_gpu_f8_linear.py, which worst cases make wide.
+
+What the bound is made of, relative, for operands of random signs (B = 2^e m, m in [1, 2)):
+  - V (U) as bf16 hi + lo: lo lies within 2^-8 2^e, evenly, 2^-8 / sqrt(3) in the mean square;
+    its own rounding is within 2^-8 of its power of two, 0.72 2^-8 / sqrt(3) of itself. Together
+    3.7e-6 2^e, or 2.5e-6 of values whose mean square is 1.44 2^e.
+  - sums in TMEM are cut off: a chain of n additions loses about n 2^-24 2 / 3 of its sum
+    (half a unit each of partial sums that grow with the square root), 2.5e-6 for 64.
+  - fp32 sums of the chains, a few 2^-24.
+In the mean square 3.6e-6: dA and dB within 4e-6.  One bf16 term alone would give 1e-3.
+"""
+
+import pytest
+import torch
+
+from bit_nf4_quantized_17_b200 import qlora as Q
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def _inputs(M, N, K, r):
+    g = torch.Generator(DEV).manual_seed(M + N + K + r)
+    rn = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    return [t.bfloat16() for t in (rn(N, K) / 50, rn(r, K) / r ** 0.5, rn(N, r) / 50, rn(M, K),
+                                   rn(M, N))]
+
+
+def _product(a, b):
+    """a^T b in fp64, a stretch of rows at a time."""
+    out = torch.zeros(a.shape[1], b.shape[1], dtype=torch.float64, device=DEV)
+    for i in range(0, a.shape[0], 4096):
+        out += a[i:i + 4096].double().t() @ b[i:i + 4096].double()
+    return out
+
+
+def _off(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+LONG = [(16384, 256, 4096, 16), (8192, 128, 11008, 32), (20001, 72, 2048, 128),
+        (65536, 136, 1032, 64), (9000, 64, 11008, 256), (33000, 64, 200, 160)]
+
+
+@pytest.mark.parametrize("M,N,K,r", LONG)
+def test_grad_a_over_many_tokens(M, N, K, r):
+    W, A, B, X, dY = _inputs(M, N, K, r)
+    w8, x8 = Q.qlora_f8_quantize(W, Q.QLORA_F8_TILES), Q.qlora_f8_quantize(X)
+    U = torch.zeros((M, r), device=DEV)
+    _, dA, _ = Q.qlora_f8_linear_bwd(w8, A, B, float(r), x8, U, dY, want_dx=False, check=True)
+    want = _product(dY.double() @ B.double(), Q.qlora_f8_dequantize(x8))
+    assert _off(dA, want) < 4e-6
+    # added to what is there, once
+    dA2 = dA.clone()
+    Q.qlora_f8_linear_bwd(w8, A, B, float(r), x8, U, dY, dA=dA2, accumulate=True, want_dx=False,
+                          dB=torch.zeros((N, r), device=DEV), check=True)
+    assert _off(dA2, 2 * want) < 4e-6
+    if K % 64 == 0:
+        q = Q.qlora_quantize(W)
+        _, dA, _ = Q.qlora_linear_bwd_f8(q, A, B, r, float(r), x8, U, dY, want_dx=False, check=True)
+        assert _off(dA, want) < 4e-6
