@@ -19,7 +19,7 @@
 // 2.0e-5 in one accumulator and launch); 2.5e-6 of it are V's two terms.  Roles (384
 // threads): warp 0 loads codes, warp 2 loads V^T, warp 1 owns TMEM and issues
 // the MMAs, warps 4-11 expand in two groups (group g takes 64-token tiles
-// i % 2 == g), warps 4-7 drain.  Every wait is bounded; a wait that gives up
+// i % 2 == g) and drain.  Every wait is bounded; a wait that gives up
 // reports QLORA_ERR_DEVICE_TIMEOUT and leaves NaN in its columns of dA.
 // Up to 16 tokens: CUDA cores, bound by writing dA; a thread takes 16 columns of 4
 // ranks, so that each code is expanded once for 4 ranks.
@@ -217,12 +217,12 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   }
   __syncthreads();
   // ---------------------------------------- partial sums to shared memory, transposed
-  if (warp >= 4 && warp < 8) {
+  if (warp >= 4) {
     const int i = 32 * (warp & 3) + lane;  // column of X in the tile
     bool ok = tn > 0 && ptx::mbar_wait(accum, 0, kTimeoutCycles, abort_flag);
     ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     if (ok) ptx::tc_fence_after();
-    for (int c = 0; c < 2 * p.rc; c += 16) {
+    for (int c = 16 * ((warp - 4) >> 2); c < 2 * p.rc; c += 32) {
       float v[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = 0.0f;
@@ -385,7 +385,8 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
   // TMEM columns of a CTA: half of them where two share an SM.  A CTA asks for at least the
   // shared memory that goes with its columns, so that no other kernel's CTA that needs TMEM
   // finds room beside it and has to wait for this one while its cluster waits for it.
-  const int max_accs = (need > kMaxSmem / 2 - 1024 ? 512 : 256) / p.acc_cols;
+  const bool two = need <= kMaxSmem / 2 - 1024;
+  const int max_accs = (two ? 256 : 512) / p.acc_cols;
   const int64_t kt_total = ceil_div(M, 64);
   const int64_t tiles = ceil_div(K, 128);
   cudaLaunchConfig_t cfg = {};
@@ -405,21 +406,31 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
     attr[0].val.clusterDim.z = static_cast<unsigned>(n);
     cfg.gridDim = dim3(static_cast<unsigned>(tiles), chunks, n);
   };
-  // Splits of the tokens, at least 4 tiles each: whichever ends soonest, launches times
-  // rounds of clusters that run at once times the tiles of one and about four for its start
-  // and sum.
-  // (Backward without dX against as many CTAs as the SMs hold: 4096 tokens x 2048 at rank
-  // 128 62.2 us, was 74.8; 2048 x 4096 at rank 64 28.4, 31.5; 8192 x 4096 at rank 16 34.8,
-  // 33.0.)
+  // Clusters of n that run at once.  The runtime answers for one CTA per SM; where an SM
+  // holds two, a group of SMs holds clusters of n as one of half their size.
+  auto at_once = [&](int n, int64_t per, bool both) -> int64_t {
+    plan(n, per);
+    const int64_t one = std::max(1, f8_resident_clusters(kernel, cfg));
+    if (!both) return one;
+    plan((n + 1) / 2, per);
+    return std::max<int64_t>(2 * one, f8_resident_clusters(kernel, cfg));
+  };
+  // Splits of the tokens, at least 4 tiles each: whichever ends soonest.  In tenths of a tile's
+  // time a launch takes 60 and, a round of clusters that run at once, 10 a tile (18 where two
+  // CTAs share an SM), 40 for the start and 6 a split for the sum.  Backward without dX, d_in
+  // 4096, rank 16, in 4 and in 8 splits: 4096 tokens 33.2 and 32.8 us, 8192 55.6 and 51.4,
+  // 16384 96.9 and 86.9; 2048 at rank 64 33.9 and 36.8; d_in 2048, rank 128, 4096 tokens, in
+  // 6 and 8 (two rounds) 64.3 and 76.9; d_in 8192, rank 256, 8192 tokens in one launch of 4
+  // and in four of 1 358 and 399.
   int splits = 1;
   int64_t least = 0, launches = 1;
   for (int n = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, kt_total / 4))); n >= 1;
        --n) {
     const int64_t times = ceil_div(kt_total, n * (kMaxChain / 4) * max_accs);
-    const int64_t per = ceil_div(ceil_div(kt_total, times), n);
-    plan(n, per);
-    const int64_t at_once = std::max(1, f8_resident_clusters(kernel, cfg));
-    const int64_t cost = times * ceil_div(tiles * chunks, at_once) * (per + 4);
+    const int64_t per = ceil_div(ceil_div(kt_total, times), n), clusters = tiles * chunks;
+    const bool both = two && clusters > at_once(n, per, false);
+    const int64_t rounds = ceil_div(clusters, at_once(n, per, both));
+    const int64_t cost = times * (rounds * (per * (both ? 18 : 10) + 40 + 6 * n) + 60);
     if (least != 0 && cost >= least) continue;
     least = cost;
     splits = n;
