@@ -2,10 +2,12 @@
 // f8_quantize.cu) and the LoRA factor U = X A^T (or V = dY B) from one read of X.
 //
 // A CTA takes 128 tokens and a share of the contraction: X and the factor's operand come
-// by TMA in 64-column tiles (128-byte swizzle).  One thread multiplies them into four TMEM
-// accumulators in turn (two above rank 128; tcgen05.mma, N = the rank rounded up): sums
-// there are cut off, not rounded, and shorter chains lose less (U of 2048 x 8192 at rank 64
-// against fp64: 3.2e-7, 1.4e-6 in one accumulator; 0.3 us).  Beside it two groups of four warps
+// by TMA in 64-column tiles (128-byte swizzle).  One thread multiplies them into several TMEM
+// accumulators in turn (tcgen05.mma, N = the rank rounded up): sums there are cut off, not
+// rounded, and shorter chains lose less (U of 2048 x 8192 at rank 64 against fp64: 3.2e-7,
+// 1.4e-6 in one accumulator; 0.3 us).  Four (two above rank 128), more as far as TMEM goes
+// where a chain were longer than 32 MMAs, and more splits where longer than 64 (16384 tokens x
+// 22016 at rank 64: 8.9e-7, 6.0e-6 in four accumulators and one split).  Beside it two groups of four warps
 // take the 128-column blocks in turn, a thread a row: the block's 64 words of X in
 // registers give its scale and codes, which leave through shared memory and TMA stores.
 // The shares are summed in distributed shared memory in order, as in gemm_rank.cu.  Every wait
@@ -36,6 +38,7 @@ constexpr int kCodeBytes = 16384;
 constexpr int kMaxStages = 8;
 constexpr int kStageBudget = 192 * 1024;
 constexpr int kMaxSmem = 1024 + kStageBudget + 2 * kCodeBytes + 256;
+constexpr int kChain = 32, kMaxChain = 64;  // MMAs into one accumulator: wanted, at most
 constexpr long long kTimeoutCycles = 4000000000ll;
 
 struct WideArgs {
@@ -377,7 +380,7 @@ qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* s
   p.stages = kMaxStages * p.stage_bytes <= kStageBudget ? kMaxStages : 4;
   p.acc_cols = 32;
   while (p.acc_cols < p.bn) p.acc_cols *= 2;
-  p.accs = p.acc_cols > 128 ? 2 : 4;
+  const int max_accs = 512 / p.acc_cols;
   p.red_ld = p.bn + 4;
   p.area = static_cast<int32_t>(
       ceil_div(std::max(p.stages * p.stage_bytes, 128 * p.red_ld * 4), 1024) * 1024);
@@ -422,12 +425,17 @@ qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* s
   if (cudaGetDevice(&dev) == cudaSuccess)
     (void)cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, sms / m_tiles, kbs / 4})));
-  for (;; --splits) {
+  // no fewer than keep a chain at kMaxChain MMAs, four a tile
+  const int least = static_cast<int>(
+      std::min<int64_t>(8, ceil_div(p.kt_total, kMaxChain / 4 * max_accs)));
+  for (splits = std::max(splits, least);; --splits) {
     attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
     cfg.gridDim = dim3(static_cast<unsigned>(m_tiles), 1u, static_cast<unsigned>(splits));
-    if (splits == 1 || m_tiles <= f8_resident_clusters(fn, cfg)) break;
+    if (splits == least || m_tiles <= f8_resident_clusters(fn, cfg)) break;
   }
   p.k_tiles = 2 * static_cast<int32_t>(ceil_div(kbs, splits));
+  for (p.accs = std::min(4, max_accs); p.accs < max_accs && 4 * p.k_tiles > kChain * p.accs;)
+    p.accs *= 2;
   void* args[] = {&mx, &mb, &mc, &p};
   count_launch();
   const int kind = f.encode ? QLORA_KERNEL_QUANTIZE : QLORA_KERNEL_LORA_GEMM;
