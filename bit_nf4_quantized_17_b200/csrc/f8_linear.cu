@@ -112,7 +112,18 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
     rb.ld1 = r;
     rb.a1 = sc;
     rb.acc1 = accumulate;
-    return rank_product(dY, true, N, M, N, ut, mp, 2 * r16, 2 * r16, part, L.split_db, rb, st, s2);
+    if (tc_rank_eligible(2 * r16, r, r16))
+      return tc_rank_gemm(dY, true, N, M, N, ut, false, mp, 2 * r16, 2 * r16, rb, st, s2, true);
+    // split-K into the workspace: 64 MMAs a chain and split at most, then the next tokens
+    const int64_t each = int64_t(1024) * L.split_db;
+    for (int64_t m0 = 0; m0 < M; m0 += each) {
+      const int64_t m = std::min(each, M - m0), tiles = ceil_div(m, 64);
+      const int splits = static_cast<int>(ceil_div(tiles, ceil_div(tiles, L.split_db)));
+      QLORA_TRY(rank_product(static_cast<const __nv_bfloat16*>(dY) + m0 * N, true, N, m, N,
+                             ut + 2 * m0, mp, 2 * r16, 2 * r16, part, splits, rb, st, s2));
+      rb.acc1 = true;
+    }
+    return QLORA_OK;
   };
   auto all_work = [&]() -> qlora_status {
     QLORA_TRY(v_work());

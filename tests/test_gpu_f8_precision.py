@@ -74,3 +74,20 @@ def test_grad_a_over_many_tokens(M, N, K, r):
         q = Q.qlora_quantize(W)
         _, dA, _ = Q.qlora_linear_bwd_f8(q, A, B, r, float(r), x8, U, dY, want_dx=False, check=True)
         assert _off(dA, want) < 4e-6 + N / 16 * 2.0 ** -24 * 2 / 3
+
+
+@pytest.mark.parametrize("M,N,K,r", [(16384, 4096, 64, 16), (65536, 1000, 64, 64),
+                                     (40001, 2048, 64, 96), (20000, 11008, 64, 128),
+                                     (9000, 22016, 64, 64), (70000, 136, 64, 200),
+                                     (33001, 4096, 64, 256)])
+def test_grad_b_over_many_tokens(M, N, K, r):
+    W, A, B, X, dY = _inputs(M, N, K, r)
+    w8, x8 = Q.qlora_f8_quantize(W, Q.QLORA_F8_TILES), Q.qlora_f8_quantize(X)
+    U = X.float() @ A.float().t()
+    _, _, dB = Q.qlora_f8_linear_bwd(w8, A, B, float(r), x8, U, dY, want_dx=False, check=True)
+    want = _product(dY, U)
+    assert _off(dB, want) < 4e-6
+    dB2 = dB.clone()
+    Q.qlora_f8_linear_bwd(w8, A, B, float(r), x8, U, dY, dB=dB2, accumulate=True, want_dx=False,
+                          dA=torch.zeros((r, K), device=DEV), check=True)
+    assert _off(dB2, 2 * want) < 4e-6
