@@ -12,6 +12,11 @@ namespace qlora {
 // Scale blocks along one axis of `n` elements.
 inline int64_t f8_blocks(int64_t n) { return ceil_div(n, 128); }
 
+// f8_gemm.cu: SMs of the current device.
+namespace f8 {
+int sm_count();
+}
+
 // abi_f8.cu: shape and pointer checks of a qlora_f8.
 qlora_status check_f8(const qlora_f8& q);
 

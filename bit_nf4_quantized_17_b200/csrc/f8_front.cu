@@ -5,14 +5,17 @@
 
 namespace qlora {
 
-// Where every warp has one block at most (16 tokens x 16 ranks x 128 columns) the launch is
-// one latency.  Forward of the layer with this kernel and with f8_front_wide's: 24 x 4096 x
-// 4096 at rank 16 11.7 and 14.6 us, 128 of them at rank 64 16.3 and 18.6, 256 18.9 and
-// 20.4.  With more blocks (256 x 8192 x 8192 at rank 64: 42.6 and 36.8) or tokens (512 x
-// 4096 x 4096 at rank 16: 27.3 and 22) reading X and A once each wins.
+// Up to 16 tokens this kernel is the faster form at any size, with f8_front_wide_kernel's rows
+// mostly empty: forward of the layer with this one and with that, one token x 4096 x 4096 at
+// rank 16 9.4 and 13.0 us, 16 x 8192 x 8192 at rank 64 14.5 and 22.5, 16 x 1024 x 20000 at
+// rank 256 21.0 and 36.2.  Up to 256 tokens it is where every warp has one block at most (16
+// tokens x 16 ranks x 128 columns), so that the launch is one latency: 24 x 4096 x 4096 at
+// rank 16 11.7 and 15.2, 128 x 4096 x 4096 at rank 64 15.4 and 18.8, 256 of them 18.6 and 20.5.
+// With more blocks (256 x 8192 x 8192 at rank 64: 39.7 and 36.5; 128 x 1024 x 8192 at rank 256:
+// 33.7 and 27.3) or tokens reading X and A once each wins.
 bool f8_front_takes(int64_t M, int64_t K, int32_t r) {
-  return M <= 16 ||
-         (M <= 256 && ceil_div(M, 16) * f8_blocks(K) * ceil_div(r, kRanks) <= 148 * kMaxWarps);
+  if (M <= 16 || M > 256) return M <= 16;
+  return ceil_div(M, 16) * f8_blocks(K) * ceil_div(r, kRanks) <= f8::sm_count() * kMaxWarps;
 }
 
 qlora_status f8_front(const FrontOp& f, const qlora_f8& x8, cudaStream_t s) {
@@ -41,12 +44,13 @@ qlora_status f8_front(const FrontOp& f, const qlora_f8& x8, cudaStream_t s) {
   const int64_t groups = p.span / kRanks;  // those past the last rank write zeros
   // a warp per 16 tokens and block of 128 columns, as far as all run at once; then
   // more tokens per CTA and more blocks per warp
+  const int64_t warps = static_cast<int64_t>(f8::sm_count()) * kMaxWarps;
   int64_t blocks;
   int slices;
   for (p.tiles = 1;; p.tiles *= 2) {
     blocks = ceil_div(M, 16 * p.tiles);
     slices = std::min(kMaxWarps / p.tiles, p.per);
-    if (p.tiles == 8 || ctas * groups * blocks * p.tiles * slices <= 148 * kMaxWarps) break;
+    if (p.tiles == 8 || ctas * groups * blocks * p.tiles * slices <= warps) break;
   }
   const bool e5 = x8.format == QLORA_E5M2, two = M > 8;
   const void* fn = f.along ? front_along_kernel(e5, two) : front_kernel<false>(e5, two);

@@ -421,9 +421,7 @@ qlora_status f8_front_wide(const FrontOp& f, const qlora_f8& x8, DeviceStatus* s
   cfg.numAttrs = 1;
   // as many splits as run at once, at least 4 blocks each
   const int64_t kbs = f8_blocks(K);
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    (void)cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = f8::sm_count();
   int splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, sms / m_tiles, kbs / 4})));
   // no fewer than keep a chain at kMaxChain MMAs, four a tile
   const int least = static_cast<int>(

@@ -124,9 +124,6 @@ static __device__ __forceinline__ void store_run(const GemmArgs& p, int64_t row,
   }
 }
 
-// SMs of the current device.
-int sm_count();
-
 // The fields of the arguments that do not depend on the kernel.
 GemmArgs gemm_args(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c, bool c_f32,
                    const F8Lora& l);

@@ -480,10 +480,7 @@ qlora_status f8_gemm_pairs(const qlora_f8& a, const qlora_f8& b, bool trans_b, v
   }
   if (regs * kThreads < 32 * (kRoleWarps * kRoleRegs + kEpi * kSumRegs))
     return QLORA_ERR_UNSUPPORTED;
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    (void)cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(tiles, sms / 2));
+  const int64_t pairs = std::max<int64_t>(1, std::min<int64_t>(tiles, f8::sm_count() / 2));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
   cfg.blockDim = dim3(kThreads);

@@ -442,12 +442,6 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uin
   return d;
 }
 
-// The same for 64-byte swizzled tiles (layout type 4).
-__device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  return (sw128_desc(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7) << 61)) |
-         (static_cast<uint64_t>(4) << 61);
-}
-
 // Instruction descriptor of kind::f16 with bf16 A and B and fp32 D.
 __host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, int a_mn_major, int b_mn_major) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(a_mn_major) << 15) |
