@@ -37,7 +37,7 @@ struct FrontOp {
   float* u;       // U (M x r fp32) or NULL
   float sc;
   void* su;       // sc U as bf16 [hi | lo], lora_span(r) columns each
-  void* ut;       // U^T as bf16 [hi ; lo], lo from row ut_lo on, rows of ut_ld; or NULL
+  void* ut;       // U^T as three bf16 terms, ut_lo rows apart, rows of ut_ld; or NULL
   int64_t ut_ld;
   int32_t ut_lo;
 };
@@ -69,8 +69,8 @@ qlora_status f8_gemm(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c
 int f8_resident_clusters(const void* fn, const cudaLaunchConfig_t& cfg);
 
 // f8_grad.cu: dA (r x d_in fp32) = sc V^T X^ from X kept by rows in 8 bits (added to
-// dA when accumulate).  More than 16 tokens: V^T as bf16 hi rows [0, r) and lo
-// rows from lora_rows(r) on, ld_v elements a row; r a multiple of 8 up to 256.  Up
+// dA when accumulate).  More than 16 tokens: V^T as three bf16 terms, lora_rows(r)
+// rows apart, ld_v elements a row; r a multiple of 8 up to 256.  Up
 // to 16 tokens: V (M x r fp32), r and d_in multiples of 8.
 qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t r, float sc,
                        bool accumulate, float* dA, DeviceStatus* st, cudaStream_t s);

@@ -1,11 +1,24 @@
 // Encoding of a block of values in 8 bits (definitions: f8_quantize.cu), for the kernels
-// that quantise.
+// that quantise, and of an fp32 value as bf16 terms.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
 namespace qlora {
+
+// An fp32 value as three bf16 terms, 24 bits in all: what each leaves is exact in fp32.
+struct Terms {
+  __nv_bfloat16 hi, mid, lo;
+};
+__device__ __forceinline__ Terms terms_of(float v) {
+  Terms t;
+  t.hi = __float2bfloat16_rn(v);
+  v -= __bfloat162float(t.hi);
+  t.mid = __float2bfloat16_rn(v);
+  t.lo = __float2bfloat16_rn(v - __bfloat162float(t.mid));
+  return t;
+}
 
 constexpr float kScaleFloor = 1.17549435e-38f;  // 2^-126
 

@@ -45,7 +45,7 @@ struct FrontArgs {
   float* u;                // M x r or NULL
   __nv_bfloat16* su;       // M x [span | span]
   float sc;
-  __nv_bfloat16* ut;       // ALONG: U^T as [hi ; lo] or NULL: rows of ut_ld, lo from row ut_lo on
+  __nv_bfloat16* ut;       // ALONG: U^T as three terms or NULL: rows of ut_ld, terms ut_lo rows apart
   int64_t ut_ld;
   int32_t ut_lo;
 };
@@ -236,9 +236,10 @@ __global__ void __launch_bounds__(32 * kMaxWarps) f8_front_kernel(const FrontArg
     const int64_t row = 16 * tile0 + m;
     if (j < p.r && p.u) p.u[row * p.r + j] = v;
     if (ALONG && j < p.r && p.ut) {
-      const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-      p.ut[j * p.ut_ld + row] = hi;
-      p.ut[(p.ut_lo + j) * p.ut_ld + row] = __float2bfloat16_rn(v - __bfloat162float(hi));
+      const Terms t = terms_of(v);
+      p.ut[j * p.ut_ld + row] = t.hi;
+      p.ut[(p.ut_lo + j) * p.ut_ld + row] = t.mid;
+      p.ut[(2 * p.ut_lo + j) * p.ut_ld + row] = t.lo;
     }
     if (j < p.span) {  // zeros past the last rank
       const float f = j < p.r ? p.sc * v : 0.0f;

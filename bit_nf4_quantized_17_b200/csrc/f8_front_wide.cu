@@ -52,7 +52,7 @@ struct WideArgs {
   float* u;                      // m x r or NULL
   __nv_bfloat16* su;             // m x [span | span]
   float sc;
-  __nv_bfloat16* ut;             // [hi ; lo] or NULL
+  __nv_bfloat16* ut;             // three terms, ut_lo rows apart, or NULL
   int64_t ut_ld;
   int32_t ut_lo;
   DeviceStatus* st;
@@ -328,10 +328,10 @@ f8_front_wide_kernel(const __grid_constant__ CUtensorMap tmX,
         if (p.ut) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(v[q]);
-            p.ut[(j + q) * p.ut_ld + row] = hi;
-            p.ut[(p.ut_lo + j + q) * p.ut_ld + row] =
-                __float2bfloat16_rn(v[q] - __bfloat162float(hi));
+            const Terms t = terms_of(v[q]);
+            p.ut[(j + q) * p.ut_ld + row] = t.hi;
+            p.ut[(p.ut_lo + j + q) * p.ut_ld + row] = t.mid;
+            p.ut[(2 * p.ut_lo + j + q) * p.ut_ld + row] = t.lo;
           }
         }
       }

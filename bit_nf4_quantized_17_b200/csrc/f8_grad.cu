@@ -9,14 +9,15 @@
 // as the restored activations would be, and no bf16 copy of X is written.
 //
 // More than 16 tokens: D = X^T V^T per 128 columns of X on the tensor cores
-// (tcgen05.mma kind::f16, M = 128, N = 2 rc), V in bf16 as hi + lo (accurate to about
-// 2^-17; rank chunks of rc <= 128), the contraction split over a cluster and
-// summed in distributed shared memory in split order, as in gemm_rank.cu.  Sums in TMEM are
-// cut off, not rounded, which adds up along a chain of MMAs: a split takes its tiles in
-// turn into as many accumulators as keep the chains at 32 MMAs (512 tokens), as far as
-// TMEM goes, and tokens past 64 MMAs a chain are a launch of their own that adds to dA.
-// Relative to fp64 at rank 16, 4096 columns: 4096 tokens 2.55e-6, 65536 3.1e-6 (2.7e-6 and
-// 2.0e-5 in one accumulator and launch); 2.5e-6 of it are V's two terms.  Roles (384
+// (tcgen05.mma kind::f16, M = 128, N = rc ranks <= 128), the contraction split over a cluster
+// and summed in distributed shared memory in split order, as in gemm_rank.cu.  V is fp32: it
+// enters as three bf16 terms (24 bits; two would leave dA off by 2.5e-6 relative).  Sums in
+// TMEM are cut off, not rounded, which adds up along a chain of MMAs: the first term's
+// products go tile by tile in turn into as many accumulators as keep its chains at 16 MMAs (256
+// tokens), as far as TMEM goes, the small products of the other two into one more, and
+// tokens past 48 MMAs a chain (64 above rank 64) are a launch of their own that adds to dA.  Relative to fp64 at
+// rank 16, 4096 columns: 4096 tokens 4.3e-7, 65536 8.8e-7 (2.7e-6 and 2.0e-5 with two terms in
+// one accumulator and launch).  Roles (384
 // threads): warp 0 loads codes, warp 2 loads V^T, warp 1 owns TMEM and issues
 // the MMAs, warps 4-11 expand in two groups (group g takes 64-token tiles
 // i % 2 == g) and drain.  Every wait is bounded; a wait that gives up
@@ -38,9 +39,23 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kABytes = 16384;     // 64 tokens x 128 columns in bf16, two 64-column halves
 constexpr int kCodeBytes = 8192;   // 64 tokens x 128 codes
+// even numbers: a slot's tiles all go to the same group, which has seen every phase of the
+// barriers that it waits on
 constexpr int kCodeSlots = 4;
 constexpr int kStages = 2;
-constexpr int kChain = 32, kMaxChain = 64;  // MMAs into one accumulator: wanted, at most
+static_assert(kCodeSlots % 2 == 0 && kStages % 2 == 0, "each slot and stage has one group");
+constexpr int kMaxVStages = 8;
+// Shared memory beside the tiles: their alignment to 1024 bytes from 128, and two words and
+// the barriers, of which those that free a stage of V are A's where both have two stages (at
+// rank 64 two CTAs then fit an SM to the byte).
+constexpr int kAlignSlack = 1024 - 128;
+constexpr int barrier_bytes(int v_stages) {
+  return 8 + 8 * (2 * kCodeSlots + 2 * kStages + 1 + (v_stages == kStages ? 1 : 2) * v_stages);
+}
+static_assert(barrier_bytes(kStages) == 128, "see above");
+constexpr int kTerms = 3;          // of V
+constexpr int kChain = 16;         // MMAs into one accumulator: wanted, and at most where two
+constexpr int kMaxChain = 48, kMaxChainAlone = 64;  // CTAs share an SM or one has it alone
 constexpr int kMaxSmem = 227 * 1024;
 constexpr int kSmemPerColumn = 228 * 1024 / 512;  // of an SM's shared memory to its TMEM columns
 constexpr long long kTimeoutCycles = 4000000000ll;
@@ -49,9 +64,10 @@ struct GradArgs {
   const float* scales;   // [kb][m]
   int32_t m, k;          // tokens, columns of X
   int32_t kt0, kt_end, kt_per;  // 64-token tiles of this launch, tiles per split
-  int32_t r, rc, lo_row;     // rank, ranks per chunk (a multiple of 16), first lo row of V^T
+  int32_t r, rc, lo_row;     // rank, ranks per chunk (a multiple of 16), rows of a term of V^T
+  int32_t v_stages;      // of V^T tiles
   int32_t area;          // bytes of the tiles (the partial sums reuse them)
-  int32_t accs, acc_cols;    // accumulators, TMEM columns of one (powers of two)
+  int32_t accs, tmem_cols;   // accumulators of the first term (a power of two), TMEM columns
   float* dA;
   float sc;
   int32_t accumulate;
@@ -75,22 +91,25 @@ template <bool E5M2>
 __global__ void __launch_bounds__(kThreads, 2)
 f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmV,
                const GradArgs p) {
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(128) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  // [kStages x (A | V^T)] [codes], reused as the fp32 partial sums
-  const int stage_bytes = kABytes + 2 * p.rc * 128;
-  uint8_t* codes = smem + kStages * stage_bytes;
-  float* red = reinterpret_cast<float*>(smem);  // [2 rc][132]: 128 columns of X each
+  // [kStages x A] [codes] [v_stages x V^T], reused as the fp32 partial sums
+  const int v_bytes = kTerms * p.rc * 128;
+  uint8_t* codes = smem + kStages * kABytes;
+  uint8_t* vtile = codes + kCodeSlots * kCodeBytes;
+  float* red = reinterpret_cast<float*>(smem);  // [rc][132]: 128 columns of X each
   constexpr int kRedLd = 132;
-  uint64_t* code_full = reinterpret_cast<uint64_t*>(smem + p.area);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + p.area);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint64_t* code_full = reinterpret_cast<uint64_t*>(tmem_slot + 2);
   uint64_t* code_empty = code_full + kCodeSlots;
   uint64_t* full_a = code_empty + kCodeSlots;
-  uint64_t* full_b = full_a + kStages;
-  uint64_t* empty = full_b + kStages;
+  uint64_t* empty = full_a + kStages;
   uint64_t* accum = empty + kStages;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(accum + 1);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint64_t* full_b = accum + 1;
+  const bool shared = p.v_stages == kStages;  // one barrier frees A's and V's stage
+  uint64_t* empty_b = shared ? empty : full_b + p.v_stages;
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t S = gridDim.z, z = blockIdx.z;
@@ -106,8 +125,11 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     }
     for (int s = 0; s < kStages; ++s) {
       ptx::mbar_init(&full_a[s], 4);
-      ptx::mbar_init(&full_b[s], 1);
       ptx::mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < p.v_stages; ++s) {
+      ptx::mbar_init(&full_b[s], 1);
+      if (!shared) ptx::mbar_init(&empty_b[s], 1);
     }
     ptx::mbar_init(accum, 1);
     *abort_flag = 0;
@@ -116,7 +138,7 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     ptx::prefetch_tmap(&tmV);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(tmem_slot, p.accs * p.acc_cols);
+    ptx::tmem_alloc(tmem_slot, p.tmem_cols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -139,38 +161,58 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     for (int i = (issued > kCodeSlots ? issued - kCodeSlots : 0); i < issued; ++i)
       ptx::mbar_wait(&code_full[i % kCodeSlots], (i / kCodeSlots) & 1, kTimeoutCycles, nullptr);
   } else if (warp == 2 && ptx::elect_one()) {
-    // ------------------------------------------------------ V^T: hi and lo rows of the chunk
-    int issued = 0;
+    // ------------------------------------------------------ V^T: the chunk's rows of each term
+    int issued = 0, s = 0;
+    uint32_t ph = 1;
     for (int i = 0; i < tn; ++i) {
-      const int s = i % kStages;
-      if (!ptx::mbar_wait(&empty[s], ((i / kStages) & 1) ^ 1, kTimeoutCycles, abort_flag)) break;
-      uint8_t* sv = smem + s * stage_bytes + kABytes;
-      ptx::mbar_arrive_expect_tx(&full_b[s], 2 * p.rc * 128);
-      ptx::tma_load_2d(&tmV, &full_b[s], sv, (t0 + i) * 64, j0);
-      ptx::tma_load_2d(&tmV, &full_b[s], sv + p.rc * 128, (t0 + i) * 64, p.lo_row + j0);
+      if (!ptx::mbar_wait(&empty_b[s], ph, kTimeoutCycles, abort_flag)) break;
+      uint8_t* sv = vtile + s * v_bytes;
+      ptx::mbar_arrive_expect_tx(&full_b[s], v_bytes);
+#pragma unroll
+      for (int t = 0; t < kTerms; ++t)
+        ptx::tma_load_2d(&tmV, &full_b[s], sv + t * p.rc * 128, (t0 + i) * 64, t * p.lo_row + j0);
       ++issued;
+      if (++s == p.v_stages) {
+        s = 0;
+        ph ^= 1;
+      }
     }
-    for (int i = (issued > kStages ? issued - kStages : 0); i < issued; ++i)
-      ptx::mbar_wait(&full_b[i % kStages], (i / kStages) & 1, kTimeoutCycles, nullptr);
+    // (none of these is more than v_stages back)
+    for (int i = (issued > p.v_stages ? issued - p.v_stages : 0); i < issued; ++i)
+      ptx::mbar_wait(&full_b[i % p.v_stages], (i / p.v_stages) & 1, kTimeoutCycles, nullptr);
   } else if (warp == 1 && ptx::elect_one()) {
     // ------------------------------------------------------ MMA issuer
+    const uint64_t term = static_cast<uint64_t>(p.rc * 128) >> 4;
+    const uint32_t rest = tmem + p.accs * p.rc;
+    // A: MN-major, two 64-column halves 8192 bytes apart, 16 tokens (2048 bytes) a step
+    const uint64_t a0 = ptx::sw128_desc(ptx::smem_u32(smem), 8192, 1024);
+    const uint64_t b0 = ptx::sw128_desc(ptx::smem_u32(vtile), 16, 1024);
+    int vs = 0;
+    uint32_t vph = 0;
+    uint64_t off = 0;
     for (int i = 0; i < tn; ++i) {
       const int s = i % kStages;
-      const uint32_t ph = (i / kStages) & 1;
-      if (!ptx::mbar_wait(&full_b[s], ph, kTimeoutCycles, abort_flag) ||
-          !ptx::mbar_wait(&full_a[s], ph, kTimeoutCycles, abort_flag))
+      if (!ptx::mbar_wait(&full_b[vs], vph, kTimeoutCycles, abort_flag) ||
+          !ptx::mbar_wait(&full_a[s], (i / kStages) & 1, kTimeoutCycles, abort_flag))
         break;
       ptx::tc_fence_after();
-      const uint32_t a_addr = ptx::smem_u32(smem + s * stage_bytes);
-      // A: MN-major, two 64-column halves 8192 bytes apart, 16 tokens (2048 bytes) a step
-      const uint64_t ad = ptx::sw128_desc(a_addr, 8192, 1024);
-      const uint64_t bd = ptx::sw128_desc(a_addr + kABytes, 16, 1024);
-      const uint32_t d = tmem + (i & (p.accs - 1)) * p.acc_cols;
+      const uint64_t ad = a0 + s * (kABytes >> 4), bd = b0 + off;
+      const uint32_t d = tmem + (i & (p.accs - 1)) * p.rc;
 #pragma unroll
-      for (int ks = 0; ks < 4; ++ks)
-        ptx::umma_bf16(d, ad + ((2048 * ks) >> 4), bd + ((32 * ks) >> 4), p.idesc,
-                       i >= p.accs || ks != 0 ? 1u : 0u);
+      for (int ks = 0; ks < 4; ++ks) {
+        const uint64_t a = ad + ((2048 * ks) >> 4), b = bd + ((32 * ks) >> 4);
+        ptx::umma_bf16(d, a, b, p.idesc, i >= p.accs || ks != 0 ? 1u : 0u);
+        ptx::umma_bf16(rest, a, b + term, p.idesc, (i | ks) != 0 ? 1u : 0u);
+        ptx::umma_bf16(rest, a, b + 2 * term, p.idesc, 1u);
+      }
       ptx::umma_commit(&empty[s]);
+      if (!shared) ptx::umma_commit(&empty_b[vs]);
+      off += v_bytes >> 4;
+      if (++vs == p.v_stages) {
+        vs = 0;
+        vph ^= 1;
+        off = 0;
+      }
     }
     ptx::umma_commit(accum);
     ptx::mbar_wait(accum, 0, kTimeoutCycles, nullptr);  // MMAs done before TMEM is freed
@@ -207,7 +249,7 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
         o[2 * q + 1] = make_uint4(e2.x, e2.y, e3.x, e3.y);
       }
       if (!ptx::mbar_wait(&empty[st], ((i / kStages) & 1) ^ 1, kTimeoutCycles, abort_flag)) break;
-      uint8_t* dst = smem + st * stage_bytes + h * 8192 + row * 128;
+      uint8_t* dst = smem + st * kABytes + h * 8192 + row * 128;
 #pragma unroll
       for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(dst + 16 * (j ^ (row & 7))) = o[j];
       ptx::fence_proxy_async_smem();
@@ -222,14 +264,16 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
     bool ok = tn > 0 && ptx::mbar_wait(accum, 0, kTimeoutCycles, abort_flag);
     ok = __all_sync(0xffffffffu, ok && !*abort_flag);
     if (ok) ptx::tc_fence_after();
-    for (int c = 16 * ((warp - 4) >> 2); c < 2 * p.rc; c += 32) {
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const int used = min(p.accs, tn);
+    for (int c = 16 * ((warp - 4) >> 2); c < p.rc; c += 32) {
       float v[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) v[j] = 0.0f;
-      for (int a = 0; ok && a < min(p.accs, tn); ++a) {
+      // the small products first
+      for (int a = used; ok && a >= 0; --a) {
         uint32_t r[16];
-        ptx::tmem_ld_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + a * p.acc_cols + c,
-                         r);
+        ptx::tmem_ld_x16(lane_base + (a == used ? p.accs : a) * p.rc + c, r);
         ptx::tmem_ld_wait(r);
 #pragma unroll
         for (int j = 0; j < 16; ++j) v[j] += __uint_as_float(r[j]);
@@ -242,10 +286,10 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   __syncthreads();
   // a wait of this CTA gave up: its sums are not whole (the status word may not be read)
   if (*abort_flag)
-    for (int e = threadIdx.x; e < 2 * p.rc * kRedLd; e += kThreads)
+    for (int e = threadIdx.x; e < p.rc * kRedLd; e += kThreads)
       red[e] = __int_as_float(0x7fffffff);
   ptx::cluster_sync();
-  // ---------------------------------------- hi + lo over the splits, in order
+  // ---------------------------------------- sum over the splits, in order
   const int cols = min(p.rc, p.r - j0);
   for (int e = static_cast<int>(z) * kThreads + threadIdx.x; e < cols * 128;
        e += static_cast<int>(S) * kThreads) {
@@ -255,8 +299,7 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
 #pragma unroll
     for (uint32_t q = 0; q < 8; ++q) {
       if (q < S) {
-        const uint32_t at = ptx::cluster_addr(red, q) + 4u * (j * kRedLd + i);
-        v += ptx::ld_cluster_f32(at) + ptx::ld_cluster_f32(at + 4u * p.rc * kRedLd);
+        v += ptx::ld_cluster_f32(ptx::cluster_addr(red, q) + 4u * (j * kRedLd + i));
       }
     }
     float* dst = p.dA + static_cast<int64_t>(j0 + j) * p.k + k0 + i;
@@ -267,7 +310,7 @@ f8_grad_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ 
   ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, p.accs * p.acc_cols);
+    ptx::tmem_dealloc(tmem, p.tmem_cols);
   }
   if (threadIdx.x == 0 && *abort_flag) report(p.st, QLORA_ERR_DEVICE_TIMEOUT, 140u);
 }
@@ -361,32 +404,39 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
   p.rc = static_cast<int32_t>(ceil_div(r16, 16 * chunks) * 16);
   CUtensorMap mx, mv;
   if (!make_map(&mx, x.codes, false, K, M, x.ld, 128, 64, true) ||
-      !make_map(&mv, vt, true, M, r16 + r, ld_v, 64, static_cast<uint32_t>(p.rc), true))
+      !make_map(&mv, vt, true, M, 2 * r16 + r, ld_v, 64, static_cast<uint32_t>(p.rc), true))
     return QLORA_ERR_CUDA;
   p.scales = x.scales;
   p.m = static_cast<int32_t>(M);
   p.k = static_cast<int32_t>(K);
   p.r = r;
   p.lo_row = r16;
-  p.area = std::max(kStages * (kABytes + 2 * p.rc * 128) + kCodeSlots * kCodeBytes,
-                    2 * p.rc * 132 * 4);
-  p.acc_cols = 32;
-  while (p.acc_cols < 2 * p.rc) p.acc_cols *= 2;
   p.dA = dA;
   p.sc = sc;
-  p.idesc = ptx::idesc_bf16(128, 2 * p.rc, 1, 0);
+  p.idesc = ptx::idesc_bf16(128, p.rc, 1, 0);
   p.st = st;
   const bool e5 = x.format == QLORA_E5M2;
   auto* fn = e5 ? f8_grad_kernel<true> : f8_grad_kernel<false>;
   const void* kernel = reinterpret_cast<const void*>(fn);
   const qlora_status cs = ensure_smem(kernel, kMaxSmem);
   if (cs != QLORA_OK) return cs;
-  const int need = 1024 + p.area + 256;
-  // TMEM columns of a CTA: half of them where two share an SM.  A CTA asks for at least the
-  // shared memory that goes with its columns, so that no other kernel's CTA that needs TMEM
-  // finds room beside it and has to wait for this one while its cluster waits for it.
-  const bool two = need <= kMaxSmem / 2 - 1024;
-  const int max_accs = (two ? 256 : 512) / p.acc_cols;
+  // Two CTAs an SM where two stages of V fit beside the rest, else one; as many stages as do
+  // (a system's 1 KB goes with each CTA).  TMEM columns likewise: half of them where two share an
+  // SM.  A CTA asks for at least the shared memory that goes with its columns, so that no
+  // other kernel's CTA that needs TMEM finds room beside it and has to wait for this one
+  // while its cluster waits for it.
+  constexpr int kFixed = kStages * kABytes + kCodeSlots * kCodeBytes;
+  const int v_bytes = kTerms * p.rc * 128;
+  auto need = [&](int stages) {
+    p.area = std::max(kFixed + stages * v_bytes, p.rc * 132 * 4);
+    return kAlignSlack + p.area + barrier_bytes(stages);
+  };
+  constexpr int kHalf = 228 * 1024 / 2 - 1024;
+  const bool two = need(kStages) <= kHalf;
+  for (p.v_stages = kMaxVStages; need(p.v_stages) > (two ? kHalf : kMaxSmem);) --p.v_stages;
+  const int smem = need(p.v_stages);
+  int max_accs = 1;
+  while ((2 * max_accs + 1) * p.rc <= (two ? 256 : 512)) max_accs *= 2;
   const int64_t kt_total = ceil_div(M, 64);
   const int64_t tiles = ceil_div(K, 128);
   cudaLaunchConfig_t cfg = {};
@@ -402,7 +452,8 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
   auto plan = [&](int n, int64_t per) {
     p.kt_per = static_cast<int32_t>(per);
     for (p.accs = 1; p.accs < max_accs && 4 * per > kChain * p.accs;) p.accs *= 2;
-    cfg.dynamicSmemBytes = std::max(need, p.accs * p.acc_cols * kSmemPerColumn - 1024);
+    for (p.tmem_cols = 32; p.tmem_cols < (p.accs + 1) * p.rc;) p.tmem_cols *= 2;
+    cfg.dynamicSmemBytes = std::max(smem, p.tmem_cols * kSmemPerColumn - 1024);
     attr[0].val.clusterDim.z = static_cast<unsigned>(n);
     cfg.gridDim = dim3(static_cast<unsigned>(tiles), chunks, n);
   };
@@ -418,15 +469,16 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
   // Splits of the tokens, at least 4 tiles each: whichever ends soonest.  In tenths of a tile's
   // time a launch takes 60 and, a round of clusters that run at once, 10 a tile (18 where two
   // CTAs share an SM), 40 for the start and 6 a split for the sum.  Backward without dX, d_in
-  // 4096, rank 16, in 4 and in 8 splits: 4096 tokens 33.2 and 32.8 us, 8192 55.6 and 51.4,
-  // 16384 96.9 and 86.9; 2048 at rank 64 33.9 and 36.8; d_in 2048, rank 128, 4096 tokens, in
-  // 6 and 8 (two rounds) 64.3 and 76.9; d_in 8192, rank 256, 8192 tokens in one launch of 4
-  // and in four of 1 358 and 399.
+  // 4096, rank 16, in 4 and in 8 splits: 4096 tokens 34.4 and 33.7 us, 8192 57.3 and 52.7;
+  // 2048 at rank 64 34.1 and 34.6; d_in 2048, rank 128, 4096 tokens, in 6 and 8 (two
+  // rounds) 66.4 and 76.6; d_in 8192, rank 256, 8192 tokens in one launch of 4 and in four of
+  // 1 437 and 470.
   int splits = 1;
   int64_t least = 0, launches = 1;
   for (int n = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, kt_total / 4))); n >= 1;
        --n) {
-    const int64_t times = ceil_div(kt_total, n * (kMaxChain / 4) * max_accs);
+    const int64_t times =
+        ceil_div(kt_total, n * ((two ? kMaxChain : kMaxChainAlone) / 4) * max_accs);
     const int64_t per = ceil_div(ceil_div(kt_total, times), n), clusters = tiles * chunks;
     const bool both = two && clusters > at_once(n, per, false);
     const int64_t rounds = ceil_div(clusters, at_once(n, per, both));

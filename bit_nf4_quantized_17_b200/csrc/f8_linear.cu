@@ -19,7 +19,7 @@ namespace {
 
 // Workspace (byte offsets; the status word is first).
 //   forward   sU [hi | lo]
-//   backward  sV [hi | lo] | V (fp32, few tokens) or V^T [hi ; lo] | U^T [hi ; lo] |
+//   backward  sV [hi | lo] | V (fp32, few tokens) or V^T (three bf16 terms) | U^T [hi ; lo] |
 //             dY codes | dY scales | split-K partials of dB (ranks above 128)
 struct Layout {
   size_t su, fwd_end;
@@ -36,7 +36,7 @@ Layout layout(int64_t M, int64_t N, int32_t r) {
   L.fwd_end = L.su + align256(2 * M * 2 * span);
   L.sv = kStatusBytes;
   L.vt = L.sv + align256(2 * M * 2 * span);
-  L.ut = L.vt + align256(std::max<size_t>(2 * 2 * r16 * mp, sizeof(float) * M * r));
+  L.ut = L.vt + align256(std::max<size_t>(2 * 3 * r16 * mp, sizeof(float) * M * r));
   L.dy_codes = L.ut + align256(2 * 2 * r16 * mp);
   L.dy_ld = ceil_div(N, 16) * 16;
   L.dy_scales = L.dy_codes + align256(M * L.dy_ld);
@@ -97,7 +97,7 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
     return cudaEventRecord(ss->fork, s) == cudaSuccess &&
            cudaStreamWaitEvent(s2, ss->fork, 0) == cudaSuccess;
   };
-  // V = dY B -> sV = s V as [hi | lo], and V (fp32) or V^T as [hi ; lo]; the 8 bits of dY
+  // V = dY B -> sV = s V as [hi | lo], and V (fp32) or V^T in terms; the 8 bits of dY
   auto v_work = [&]() -> qlora_status {
     const FrontOp f{dY, B, r, true, dX != nullptr, small ? v : nullptr, sc, sv,
                     small ? nullptr : vt, mp, r16};

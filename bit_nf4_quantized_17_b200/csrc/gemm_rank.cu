@@ -31,6 +31,7 @@
 
 #include <algorithm>
 
+#include "f8_codec.cuh"
 #include "internal.cuh"
 #include "kernels.cuh"
 #include "tc_common.cuh"
@@ -74,7 +75,7 @@ struct RankArgs {
   DeviceStatus* st;
 };
 
-template <bool SHORT>
+template <bool SHORT, bool THIRD>
 __global__ void __launch_bounds__(kThreads, 1)
 rank_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const RankArgs p) {
@@ -271,6 +272,9 @@ rank_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
         tc::reduce_store(x, gi, j + u, o.o1, o.ld1, o.trans1 ? 1 : 0, o.a1, o.acc1 ? 1 : 0,
                          static_cast<__nv_bfloat16*>(o.o2), o.ld2, o.a2, o.o2_lo,
                          static_cast<__nv_bfloat16*>(o.o3), o.ld3, o.a3, o.o3_lo);
+        if (THIRD)
+          static_cast<__nv_bfloat16*>(o.o3)[(j + u + 2 * o.o3_lo) * o.ld3 + gi] =
+              terms_of(o.a3 * x).lo;
       }
     }
     if (o.o2 && o.o2_pad && (cols % 8) == 0 && (o.o2_lo % 8) == 0 && (o.ld2 % 8) == 0 &&
@@ -344,7 +348,7 @@ int tc_rank_splits(int64_t m_tiles, int64_t k_tiles) {
 qlora_status tc_rank_gemm(const void* A, bool a_mn, int64_t m_rows, int64_t kdim, int64_t ld_a,
                           const void* B, bool b_mn, int64_t ld_b, int32_t b_rows, int32_t n_cols,
                           const ReduceArgs& out, DeviceStatus* st, cudaStream_t s,
-                          bool short_chains) {
+                          bool short_chains, bool third) {
   if (!tc_rank_eligible(n_cols, out.cols, out.lo) || m_rows < 1 || kdim < 1)
     return QLORA_ERR_UNSUPPORTED;
   // an MN-major B is read in 64-column boxes: n_cols a multiple of 64
@@ -382,8 +386,10 @@ qlora_status tc_rank_gemm(const void* A, bool a_mn, int64_t m_rows, int64_t kdim
   if (smem > 200 * 1024) return QLORA_ERR_UNSUPPORTED;
   // the limit is raised once to what any launch of this kernel may use, so
   // that the occupancy query below prices this launch's own size
-  const void* fn = short_chains ? reinterpret_cast<const void*>(rank_gemm_kernel<true>)
-                                : reinterpret_cast<const void*>(rank_gemm_kernel<false>);
+  if (third && (short_chains || !out.o3 || !out.o3_lo)) return QLORA_ERR_UNSUPPORTED;
+  const void* fn = short_chains ? reinterpret_cast<const void*>(rank_gemm_kernel<true, false>)
+                   : third      ? reinterpret_cast<const void*>(rank_gemm_kernel<false, true>)
+                                : reinterpret_cast<const void*>(rank_gemm_kernel<false, false>);
   const qlora_status cs = ensure_smem(fn, short_chains ? kMaxSmem : 200 * 1024);
   if (cs != QLORA_OK) return cs;
   // the largest shared-memory carveout, so that two CTAs fit on an SM (the

@@ -190,7 +190,8 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, int32_t r) {
 }
 
 size_t f8_input_bytes(int64_t M, int64_t N, int64_t K, int32_t r) {
-  return use_tc(M, N, K, r) ? 0 : align256(2 * M * K);
+  if (!use_tc(M, N, K, r)) return align256(2 * M * K);
+  return use_small(M) ? 0 : align256(2 * 3 * lora_rows(r) * pad8(M));
 }
 
 bool linear_multi_supported(int64_t M, int64_t N, int64_t K, int32_t r) {
@@ -392,12 +393,15 @@ qlora_status linear_backward(const qlora_nf4& W, const LevelTable& t, const void
         ra.ld1 = r;
         ra.a1 = 1.0f;
       }
-      ra.o3 = vt;
+      ra.o3 = o.x8 ? o.x_buf : vt;
       ra.ld3 = mp;
       ra.a3 = 1.0f;
       ra.o3_lo = r16;
       if (v_direct) {
-        QLORA_TRY(tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s));
+        QLORA_TRY(tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s, false,
+                               o.x8 != nullptr));
+      } else if (o.x8) {
+        return QLORA_ERR_UNSUPPORTED;  // V in three terms is the direct form's
       } else {
         QLORA_TRY(rank_product(dY, false, M, N, N, bt, N, r, r16, part, sp.v, ra, st, s));
       }
@@ -435,7 +439,7 @@ qlora_status linear_backward(const qlora_nf4& W, const LevelTable& t, const void
         QLORA_TRY(rank_product(dY, true, N, M, N, ut, mp, 2 * r16, 2 * r16, part, sp.db, ra, st,
                                s2));
       }
-      if (o.x8) return f8_grad_a(vt, mp, *o.x8, r, sc * o.keep, accumulate, dA, st, s2);
+      if (o.x8) return f8_grad_a(o.x_buf, mp, *o.x8, r, sc * o.keep, accumulate, dA, st, s2);
       // dA = s V^T X: rows d_in, stored transposed as r x d_in
       ReduceArgs ra = reduce_args(part, sp.da, K, r, 2 * r16);
       ra.lo = r16;

@@ -47,8 +47,8 @@ LinearPlan plan_linear(int64_t M, int64_t N, int64_t K, int32_t r);
 //    keep = 1 / (1 - p), and the LoRA part of dX is masked by D (mask != nullptr).
 //    Without dropout x_drop = X, keep = 1 and mask = nullptr.
 //  - Input kept in 8 bits (backward only): dA reads x8 instead of X (or of
-//    x_drop, whose kept form it then is); the CUDA-core path restores it into
-//    x_buf (M x K bf16), the tensor-core paths do not use that.
+//    x_drop, whose kept form it then is); x_buf is for the CUDA-core path to
+//    restore it (M x K bf16), and above 16 tokens on the tensor cores for V^T.
 struct LoraOpts {
   int32_t r_adapter;
   const int32_t* seg;
@@ -61,8 +61,7 @@ struct LoraOpts {
 
 bool linear_multi_supported(int64_t M, int64_t N, int64_t K, int32_t r);
 
-// Bytes behind the backward's workspace for an M x K input that is kept in 8 bits
-// (none on the tensor-core paths).
+// Bytes behind the backward's workspace for an M x K input that is kept in 8 bits (x_buf).
 size_t f8_input_bytes(int64_t M, int64_t N, int64_t K, int32_t r);
 
 // f8_linear.cu: the layer over an 8-bit base (tiles).  r, N and K multiples of 8.

@@ -1,15 +1,19 @@
 """GPU: how close the fp32 outputs of the 8-bit layers are to fp64 as a whole, in the norm,
 beside the bounds per element of test_gpu_f8_linear.py, which worst cases make wide.
 
-What the bound is made of, relative, for operands of random signs (B = 2^e m, m in [1, 2)):
-  - V (U) as bf16 hi + lo: lo lies within 2^-8 2^e, evenly, 2^-8 / sqrt(3) in the mean square;
-    its own rounding is within 2^-8 of its power of two, 0.72 2^-8 / sqrt(3) of itself. Together
-    3.7e-6 2^e, or 2.5e-6 of values whose mean square is 1.44 2^e.
+What the bounds are made of, relative, for operands of random signs (B = 2^e m, m in [1, 2)):
+  - dA reads V as three bf16 terms, 24 bits: as good as fp32.
+  - dB reads U as bf16 hi + lo: lo lies within 2^-8 2^e, evenly, 2^-8 / sqrt(3) in the mean
+    square; its own rounding is within 2^-8 of its power of two, 0.72 2^-8 / sqrt(3) of itself.
+    Together 3.7e-6 2^e, or 2.5e-6 of values whose mean square is 1.44 2^e.
   - sums in TMEM are cut off: a chain of n additions loses about n 2^-24 2 / 3 of its sum
-    (half a unit each of partial sums that grow with the square root), 2.5e-6 for 64.
+    (half a unit each of partial sums that grow with the square root), 2.5e-6 for the
+    longest, 64, and 0.64e-6 for 16.
   - fp32 sums of the chains, a few 2^-24.
-In the mean square 3.6e-6: dA and dB within 4e-6.  One bf16 term alone would give 1e-3.
-U has the sums only: 2.5e-6 and a few 2^-24, within 3e-6.
+U has the sums only: 2.5e-6 and a few 2^-24, within 3e-6.  dA has those of V and its own, dB
+its own and U's terms: in the mean square 3.6e-6, within 4e-6 over any length.  Over 256 columns
+(V: 16 additions in turn into two accumulators or more) and so few tokens that dA's chains end at
+16, within 1.2e-6, which two terms of V do not reach.
 """
 
 import pytest
@@ -50,6 +54,23 @@ def test_factor_over_many_columns(M, K, r):
     w8, U = Q.qlora_f8_quantize(W, Q.QLORA_F8_TILES), torch.empty((M, r), device=DEV)
     Q.qlora_f8_linear_fwd(w8, A, B, float(r), X, Q.F8Matrix.empty(M, K), U_save=U, check=True)
     assert _off(U, X.double() @ A.double().t()) < 3e-6
+
+
+SHORT = [(2048, 256, 4096, 16), (1000, 64, 1024, 64), (1024, 200, 1024, 128), (300, 256, 2048, 24),
+         (17, 256, 704, 256)]
+
+
+@pytest.mark.parametrize("M,N,K,r", SHORT)
+def test_grad_a_reads_all_of_v(M, N, K, r):
+    W, A, B, X, dY = _inputs(M, N, K, r)
+    w8, x8 = Q.qlora_f8_quantize(W, Q.QLORA_F8_TILES), Q.qlora_f8_quantize(X)
+    want = _product(dY.double() @ B.double(), Q.qlora_f8_dequantize(x8))
+    U = torch.zeros((M, r), device=DEV)
+    _, dA, _ = Q.qlora_f8_linear_bwd(w8, A, B, float(r), x8, U, dY, check=True)
+    assert _off(dA, want) < 1.2e-6
+    q = Q.qlora_quantize(W)
+    _, dA, _ = Q.qlora_linear_bwd_f8(q, A, B, r, float(r), x8, U, dY, check=True)
+    assert _off(dA, want) < 1.2e-6
 
 
 LONG = [(16384, 256, 4096, 16), (16384, 22016, 256, 64), (8192, 128, 11008, 32), (20001, 72, 2048, 128),
