@@ -68,6 +68,13 @@ qlora_status f8_gemm(const qlora_f8& a, const qlora_f8& b, bool trans_b, void* c
 // within one group of SMs: of size 8 at one CTA per SM fewer than 16 do.
 int f8_resident_clusters(const void* fn, const cudaLaunchConfig_t& cfg);
 
+// f8_grad_b.cu: dB (N x r fp32) = sc dY^T U (added to dB when accumulate), dY M x N bf16, U
+// M x r fp32, r and N multiples of 8.  ut: room for U^T as three bf16 terms, lora_rows(r) rows
+// each of ld_u elements (a multiple of 8, at least M).
+qlora_status f8_grad_b(const void* dY, int64_t N, const float* U, int64_t M, int32_t r, float sc,
+                       bool accumulate, void* ut, int64_t ld_u, float* dB, DeviceStatus* st,
+                       cudaStream_t s);
+
 // f8_grad.cu: dA (r x d_in fp32) = sc V^T X^ from X kept by rows in 8 bits (added to
 // dA when accumulate).  More than 16 tokens: V^T as three bf16 terms, lora_rows(r)
 // rows apart, ld_v elements a row; r a multiple of 8 up to 256.  Up

@@ -29,6 +29,7 @@
 #include <algorithm>
 
 #include "f8.cuh"
+#include "f8_splits.cuh"
 #include "linear.cuh"
 #include "tc_common.cuh"
 #include "tc_ptx.cuh"
@@ -54,10 +55,6 @@ constexpr int barrier_bytes(int v_stages) {
 }
 static_assert(barrier_bytes(kStages) == 128, "see above");
 constexpr int kTerms = 3;          // of V
-constexpr int kChain = 16;         // MMAs into one accumulator: wanted, and at most where two
-constexpr int kMaxChain = 48, kMaxChainAlone = 64;  // CTAs share an SM or one has it alone
-constexpr int kMaxSmem = 227 * 1024;
-constexpr int kSmemPerColumn = 228 * 1024 / 512;  // of an SM's shared memory to its TMEM columns
 constexpr long long kTimeoutCycles = 4000000000ll;
 
 struct GradArgs {
@@ -418,22 +415,18 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
   const bool e5 = x.format == QLORA_E5M2;
   auto* fn = e5 ? f8_grad_kernel<true> : f8_grad_kernel<false>;
   const void* kernel = reinterpret_cast<const void*>(fn);
-  const qlora_status cs = ensure_smem(kernel, kMaxSmem);
+  const qlora_status cs = ensure_smem(kernel, kCtaMaxSmem);
   if (cs != QLORA_OK) return cs;
-  // Two CTAs an SM where two stages of V fit beside the rest, else one; as many stages as do
-  // (a system's 1 KB goes with each CTA).  TMEM columns likewise: half of them where two share an
-  // SM.  A CTA asks for at least the shared memory that goes with its columns, so that no
-  // other kernel's CTA that needs TMEM finds room beside it and has to wait for this one
-  // while its cluster waits for it.
+  // Two CTAs an SM where two stages of V fit beside the rest, else one; as many stages as do.
+  // TMEM columns likewise: half of them where two share an SM.
   constexpr int kFixed = kStages * kABytes + kCodeSlots * kCodeBytes;
   const int v_bytes = kTerms * p.rc * 128;
   auto need = [&](int stages) {
     p.area = std::max(kFixed + stages * v_bytes, p.rc * 132 * 4);
     return kAlignSlack + p.area + barrier_bytes(stages);
   };
-  constexpr int kHalf = 228 * 1024 / 2 - 1024;
-  const bool two = need(kStages) <= kHalf;
-  for (p.v_stages = kMaxVStages; need(p.v_stages) > (two ? kHalf : kMaxSmem);) --p.v_stages;
+  const bool two = need(kStages) <= kCtaHalfSmem;
+  for (p.v_stages = kMaxVStages; need(p.v_stages) > (two ? kCtaHalfSmem : kCtaMaxSmem);) --p.v_stages;
   const int smem = need(p.v_stages);
   int max_accs = 1;
   while ((2 * max_accs + 1) * p.rc <= (two ? 256 : 512)) max_accs *= 2;
@@ -457,15 +450,6 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
     attr[0].val.clusterDim.z = static_cast<unsigned>(n);
     cfg.gridDim = dim3(static_cast<unsigned>(tiles), chunks, n);
   };
-  // Clusters of n that run at once.  The runtime answers for one CTA per SM; where an SM
-  // holds two, a group of SMs holds clusters of n as one of half their size.
-  auto at_once = [&](int n, int64_t per, bool both) -> int64_t {
-    plan(n, per);
-    const int64_t one = std::max(1, f8_resident_clusters(kernel, cfg));
-    if (!both) return one;
-    plan((n + 1) / 2, per);
-    return std::max<int64_t>(2 * one, f8_resident_clusters(kernel, cfg));
-  };
   // Splits of the tokens, at least 4 tiles each: whichever ends soonest.  In tenths of a tile's
   // time a launch takes 60 and, a round of clusters that run at once, 10 a tile (18 where two
   // CTAs share an SM), 40 for the start and 6 a split for the sum.  Backward without dX, d_in
@@ -474,20 +458,9 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
   // rounds) 66.4 and 76.6; d_in 8192, rank 256, 8192 tokens in one launch of 4 and in four of
   // 1 437 and 470.
   int splits = 1;
-  int64_t least = 0, launches = 1;
-  for (int n = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(8, kt_total / 4))); n >= 1;
-       --n) {
-    const int64_t times =
-        ceil_div(kt_total, n * ((two ? kMaxChain : kMaxChainAlone) / 4) * max_accs);
-    const int64_t per = ceil_div(ceil_div(kt_total, times), n), clusters = tiles * chunks;
-    const bool both = two && clusters > at_once(n, per, false);
-    const int64_t rounds = ceil_div(clusters, at_once(n, per, both));
-    const int64_t cost = times * (rounds * (per * (both ? 18 : 10) + 40 + 6 * n) + 60);
-    if (least != 0 && cost >= least) continue;
-    least = cost;
-    splits = n;
-    launches = times;
-  }
+  int64_t launches = 1;
+  choose_splits(kernel, cfg, tiles * chunks, kt_total, 4, two, max_accs, SplitCost{17, 40, 6, 60},
+                plan, &splits, &launches);
   const int64_t each = ceil_div(kt_total, launches);
   plan(splits, ceil_div(each, splits));
   for (int64_t kt0 = 0; kt0 < kt_total; kt0 += each) {

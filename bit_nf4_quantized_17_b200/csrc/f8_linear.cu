@@ -19,13 +19,12 @@ namespace {
 
 // Workspace (byte offsets; the status word is first).
 //   forward   sU [hi | lo]
-//   backward  sV [hi | lo] | V (fp32, few tokens) or V^T (three bf16 terms) | U^T [hi ; lo] |
-//             dY codes | dY scales | split-K partials of dB (ranks above 128)
+//   backward  sV [hi | lo] | V (fp32, few tokens) or V^T (three bf16 terms) |
+//             U^T (three bf16 terms) | dY codes | dY scales
 struct Layout {
   size_t su, fwd_end;
-  size_t sv, vt, ut, dy_codes, dy_scales, part, bwd_end;
+  size_t sv, vt, ut, dy_codes, dy_scales, bwd_end;
   int64_t dy_ld;
-  int split_db;
 };
 
 Layout layout(int64_t M, int64_t N, int32_t r) {
@@ -37,13 +36,10 @@ Layout layout(int64_t M, int64_t N, int32_t r) {
   L.sv = kStatusBytes;
   L.vt = L.sv + align256(2 * M * 2 * span);
   L.ut = L.vt + align256(std::max<size_t>(2 * 3 * r16 * mp, sizeof(float) * M * r));
-  L.dy_codes = L.ut + align256(2 * 2 * r16 * mp);
+  L.dy_codes = L.ut + align256(2 * 3 * r16 * mp);
   L.dy_ld = ceil_div(N, 16) * 16;
   L.dy_scales = L.dy_codes + align256(M * L.dy_ld);
-  L.part = L.dy_scales + align256(sizeof(float) * f8_blocks(N) * M);
-  L.split_db = tc_split_count(ceil_div(N, 128), ceil_div(M, 64));
-  const bool one_launch = 2 * r16 <= 256;
-  L.bwd_end = L.part + (one_launch ? 0 : align256(sizeof(float) * 2 * r16 * L.split_db * N));
+  L.bwd_end = L.dy_scales + align256(sizeof(float) * f8_blocks(N) * M);
   return L;
 }
 
@@ -84,7 +80,6 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
   auto* st = reinterpret_cast<DeviceStatus*>(ws);
   char *sv = ws + L.sv, *vt = ws + L.vt, *ut = ws + L.ut;
   float* v = reinterpret_cast<float*>(vt);  // few tokens: V in fp32
-  float* part = reinterpret_cast<float*>(ws + L.part);
   const bool small = M <= kSmallM;
   const qlora_f8 dy8{M, N, L.dy_ld, QLORA_F8_ROWS, grad_format, x8.pow2, 0,
                      reinterpret_cast<uint8_t*>(ws + L.dy_codes),
@@ -105,25 +100,7 @@ qlora_status f8_linear_backward(const qlora_f8& W, const void* A, const void* B,
   };
   auto grad_b = [&]() -> qlora_status {
     if (small) return small_grad_b(dY, U, static_cast<int>(M), N, r, sc, accumulate, dB, s2);
-    QLORA_TRY(transpose_to_bf16(U, true, M, r, r, ut, mp, r16, s2));
-    ReduceArgs rb = reduce_args(part, L.split_db, N, r, 2 * r16);
-    rb.lo = r16;
-    rb.o1 = dB;
-    rb.ld1 = r;
-    rb.a1 = sc;
-    rb.acc1 = accumulate;
-    if (tc_rank_eligible(2 * r16, r, r16))
-      return tc_rank_gemm(dY, true, N, M, N, ut, false, mp, 2 * r16, 2 * r16, rb, st, s2, true);
-    // split-K into the workspace: 64 MMAs a chain and split at most, then the next tokens
-    const int64_t each = int64_t(1024) * L.split_db;
-    for (int64_t m0 = 0; m0 < M; m0 += each) {
-      const int64_t m = std::min(each, M - m0), tiles = ceil_div(m, 64);
-      const int splits = static_cast<int>(ceil_div(tiles, ceil_div(tiles, L.split_db)));
-      QLORA_TRY(rank_product(static_cast<const __nv_bfloat16*>(dY) + m0 * N, true, N, m, N,
-                             ut + 2 * m0, mp, 2 * r16, 2 * r16, part, splits, rb, st, s2));
-      rb.acc1 = true;
-    }
-    return QLORA_OK;
+    return f8_grad_b(dY, N, U, M, r, sc, accumulate, ut, mp, dB, st, s2);
   };
   auto all_work = [&]() -> qlora_status {
     QLORA_TRY(v_work());

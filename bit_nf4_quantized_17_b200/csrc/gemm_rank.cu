@@ -16,20 +16,12 @@
 // callers need (fp32, bf16 [hi | lo] pairs, transposed copies), so no partial
 // reaches global memory and no separate reduce launch follows.
 //
-// Sums in TMEM are cut off, not rounded, which adds up along a chain of MMAs.  With
-// short_chains (dB of the layer over an 8-bit base, over any number of tokens) a split takes
-// its tiles in turn into several accumulators, and a contraction past 64 MMAs a chain is
-// several launches that add: 65536 tokens x 4096 at rank 16 2.65e-6 relative to fp64,
-// 1.9e-5 in one accumulator.
-//
 // Roles (192 threads): warp 0 TMA producer, warp 1 TMEM owner and MMA issuer,
 // warps 2-5 drain the accumulator into shared memory and reduce.  Every wait
 // on an mbarrier is bounded; a wait that gives up raises the CTA's abort flag,
 // the CTA still takes part in both cluster barriers (writing zeros), and
 // QLORA_ERR_DEVICE_TIMEOUT is reported.
 #include <cudaTypedefs.h>
-
-#include <algorithm>
 
 #include "f8_codec.cuh"
 #include "internal.cuh"
@@ -45,9 +37,6 @@ constexpr int kABytes = 16384;               // 128 rows x 64 bf16
 // stages of A and B tiles (the reduce buffer reuses them): small enough for
 // two CTAs per SM where the partial tile allows, for bytes in flight
 constexpr int kSmemBudget = 100 * 1024;
-constexpr int kChain = 32, kMaxChain = 64;   // short chains: MMAs wanted, at most
-constexpr int kMaxSmem = 227 * 1024;
-constexpr int kSmemPerColumn = 228 * 1024 / 512;  // of an SM's shared memory to its TMEM columns
 constexpr long long kTimeoutCycles = 4000000000ll;
 
 // fp32 load from another CTA's shared memory (a shared::cluster address);
@@ -68,14 +57,12 @@ struct RankArgs {
   int32_t b_mn;          // B stored MN-major (its n_cols columns contiguous): bn / 64 boxes
   int32_t bn;            // MMA N: columns of the partial tile (multiple of 16, <= 256)
   int32_t b_bytes, stage_bytes, stages, tmem_cols;
-  int32_t kt_first;      // short chains: first k-tile of this launch (kt_total: one past the last),
-  int32_t accs;          // accumulators of tmem_cols columns each (a power of two)
   int32_t red_ld;        // fp32 row stride of the shared-memory partial tile
   ReduceArgs o;          // outputs; o.part and o.splits are not used
   DeviceStatus* st;
 };
 
-template <bool SHORT, bool THIRD>
+template <bool THIRD>  // a third bf16 term for o3
 __global__ void __launch_bounds__(kThreads, 1)
 rank_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const RankArgs p) {
@@ -101,7 +88,7 @@ rank_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   const uint32_t z = ptx::cluster_ctarank();          // == blockIdx.z (cluster spans z)
   const int m0 = blockIdx.y * 128;
   const int n0 = blockIdx.x * p.bn;
-  const int kt0 = (SHORT ? p.kt_first : 0) + static_cast<int>(z) * p.k_tiles;
+  const int kt0 = static_cast<int>(z) * p.k_tiles;
   const int kn = max(0, min(p.k_tiles, p.kt_total - kt0));
 
   if (threadIdx.x == 0) {
@@ -116,7 +103,7 @@ rank_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     ptx::prefetch_tmap(&tmB);
   }
   if (warp == 1) {
-    ptx::tmem_alloc(tmem_slot, SHORT ? p.accs * p.tmem_cols : p.tmem_cols);
+    ptx::tmem_alloc(tmem_slot, p.tmem_cols);
     ptx::tmem_relinquish();
   }
   ptx::tc_fence_before();
@@ -170,11 +157,9 @@ rank_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
                                  : ptx::sw128_desc(b_addr, 16, 1024);
       const uint64_t a_step = p.a_mn ? (2048 >> 4) : (32 >> 4);
       const uint64_t b_step = p.b_mn ? (2048 >> 4) : (32 >> 4);
-      const uint32_t d = SHORT ? tmem + (i & (p.accs - 1)) * p.tmem_cols : tmem;
-      const int first = SHORT ? p.accs : 1;  // tiles that begin an accumulator
 #pragma unroll
       for (int ks = 0; ks < 4; ++ks)
-        ptx::umma_bf16(d, a0 + a_step * ks, b0 + b_step * ks, idesc, i >= first || ks ? 1u : 0u);
+        ptx::umma_bf16(tmem, a0 + a_step * ks, b0 + b_step * ks, idesc, (i | ks) != 0 ? 1u : 0u);
       ptx::umma_commit(&empty[s]);
     }
     ptx::umma_commit(accum);
@@ -190,18 +175,9 @@ rank_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
     if (ok) ptx::tc_fence_after();
     for (int c = 0; c < p.bn / 16; ++c) {
       uint32_t r[16];
-      const uint32_t at = tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 16 * c;
       if (ok) {
-        ptx::tmem_ld_x16(at, r);
+        ptx::tmem_ld_x16(tmem + (static_cast<uint32_t>(32 * quarter) << 16) + 16 * c, r);
         ptx::tmem_ld_wait();
-      }
-      for (int a = 1; SHORT && ok && a < min(p.accs, kn); ++a) {
-        uint32_t more[16];
-        ptx::tmem_ld_x16(at + a * p.tmem_cols, more);
-        ptx::tmem_ld_wait(more);
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-          r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float(more[j]));
       }
       float* dst = red + static_cast<size_t>(row) * p.red_ld + 16 * c;
 #pragma unroll
@@ -312,7 +288,7 @@ rank_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant_
   ptx::cluster_sync();
   if (warp == 1) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, SHORT ? p.accs * p.tmem_cols : p.tmem_cols);
+    ptx::tmem_dealloc(tmem, p.tmem_cols);
   }
   if (threadIdx.x == 0 && *abort_flag) report(p.st, QLORA_ERR_DEVICE_TIMEOUT, 130u);
 }
@@ -348,13 +324,12 @@ int tc_rank_splits(int64_t m_tiles, int64_t k_tiles) {
 qlora_status tc_rank_gemm(const void* A, bool a_mn, int64_t m_rows, int64_t kdim, int64_t ld_a,
                           const void* B, bool b_mn, int64_t ld_b, int32_t b_rows, int32_t n_cols,
                           const ReduceArgs& out, DeviceStatus* st, cudaStream_t s,
-                          bool short_chains, bool third) {
+                          bool third) {
   if (!tc_rank_eligible(n_cols, out.cols, out.lo) || m_rows < 1 || kdim < 1)
     return QLORA_ERR_UNSUPPORTED;
   // an MN-major B is read in 64-column boxes: n_cols a multiple of 64
   if (b_mn && n_cols % 64 != 0) return QLORA_ERR_UNSUPPORTED;
-  // launches that add: to o1 alone
-  if (short_chains && (!out.o1 || out.o2 || out.o3)) return QLORA_ERR_UNSUPPORTED;
+  if (third && (!out.o3 || !out.o3_lo)) return QLORA_ERR_UNSUPPORTED;
   CUtensorMap ma, mb;
   bool ok = a_mn ? make_map(&ma, A, true, m_rows, kdim, ld_a, 64, 64, true)
                  : make_map(&ma, A, true, kdim, m_rows, ld_a, 64, 128, true);
@@ -366,6 +341,7 @@ qlora_status tc_rank_gemm(const void* A, bool a_mn, int64_t m_rows, int64_t kdim
   p.kt_total = static_cast<int32_t>(ceil_div(kdim, 64));
   const int64_t m_tiles = ceil_div(m_rows, 128);
   int splits = tc_rank_splits(m_tiles, p.kt_total);
+  p.k_tiles = static_cast<int32_t>(ceil_div(p.kt_total, splits));
   p.a_mn = a_mn ? 1 : 0;
   p.b_mn = b_mn ? 1 : 0;
   p.bn = n_cols;
@@ -375,8 +351,6 @@ qlora_status tc_rank_gemm(const void* A, bool a_mn, int64_t m_rows, int64_t kdim
   if (p.stages > 8) p.stages = 8;
   if (p.stages < 3) p.stages = 3;  // wide partial tiles: one CTA per SM
   p.tmem_cols = pow2_at_least(n_cols);
-  p.kt_first = 0;
-  p.accs = 1;
   p.red_ld = n_cols + 4;
   p.o = out;
   p.st = st;
@@ -386,11 +360,9 @@ qlora_status tc_rank_gemm(const void* A, bool a_mn, int64_t m_rows, int64_t kdim
   if (smem > 200 * 1024) return QLORA_ERR_UNSUPPORTED;
   // the limit is raised once to what any launch of this kernel may use, so
   // that the occupancy query below prices this launch's own size
-  if (third && (short_chains || !out.o3 || !out.o3_lo)) return QLORA_ERR_UNSUPPORTED;
-  const void* fn = short_chains ? reinterpret_cast<const void*>(rank_gemm_kernel<true, false>)
-                   : third      ? reinterpret_cast<const void*>(rank_gemm_kernel<false, true>)
-                                : reinterpret_cast<const void*>(rank_gemm_kernel<false, false>);
-  const qlora_status cs = ensure_smem(fn, short_chains ? kMaxSmem : 200 * 1024);
+  auto* kernel = third ? rank_gemm_kernel<true> : rank_gemm_kernel<false>;
+  const void* fn = reinterpret_cast<const void*>(kernel);
+  const qlora_status cs = ensure_smem(fn, 200 * 1024);
   if (cs != QLORA_OK) return cs;
   // the largest shared-memory carveout, so that two CTAs fit on an SM (the
   // driver would otherwise size the carveout for one) - once per device
@@ -415,52 +387,27 @@ qlora_status tc_rank_gemm(const void* A, bool a_mn, int64_t m_rows, int64_t kdim
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // Short chains: up to half of the TMEM columns where two CTAs share an SM, and splits past
-  // those that run at once rather than launches (backward without dX of 16384 tokens, d_out
-  // 22016, rank 64: 356 us, 507 in launches of 2048 tokens, 313 with dB in one chain).
-  const int max_accs = short_chains ? (smem > kMaxSmem / 2 - 1024 ? 512 : 256) / p.tmem_cols : 1;
-  const int64_t share = kMaxChain / 4 * max_accs;  // k-tiles
-  const int least = short_chains
-                        ? static_cast<int>(std::min<int64_t>(8, ceil_div(p.kt_total, share))) : 1;
   // fewer splits while the clusters would not all be resident at once
-  if (splits < least) splits = least;
-  while (splits > least) {
+  while (splits > 1) {
     attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
     cfg.gridDim = dim3(1u, static_cast<unsigned>(m_tiles), static_cast<unsigned>(splits));
     int resident = 0;
-    if (cudaOccupancyMaxActiveClusters(&resident, fn, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&resident, kernel, &cfg) != cudaSuccess) {
       (void)cudaGetLastError();
       break;
     }
     if (static_cast<int64_t>(resident) >= m_tiles) break;
     splits -= 1;
   }
+  p.k_tiles = static_cast<int32_t>(ceil_div(p.kt_total, splits));
   cfg.gridDim = dim3(1u, static_cast<unsigned>(m_tiles), static_cast<unsigned>(splits));
   attr[0].val.clusterDim.z = static_cast<unsigned>(splits);
-  const int64_t kt_total = p.kt_total;
-  int64_t each = kt_total;
-  if (short_chains) {
-    each = ceil_div(kt_total, ceil_div(kt_total, splits * share));
-    while (p.accs < max_accs && 4 * ceil_div(each, splits) > kChain * p.accs) p.accs *= 2;
-    // at least the shared memory that goes with a CTA's columns (see f8_grad.cu)
-    cfg.dynamicSmemBytes =
-        std::max<size_t>(smem, p.accs * p.tmem_cols * kSmemPerColumn - 1024);
-  }
-  p.k_tiles = static_cast<int32_t>(ceil_div(each, splits));
-  for (int64_t kt = 0; kt < kt_total; kt += each) {
-    p.kt_first = static_cast<int32_t>(kt);
-    p.kt_total = static_cast<int32_t>(std::min(kt_total, kt + each));
-    if (kt > 0) p.o.acc1 = true;
-    count_launch();
-    timing_mark(QLORA_KERNEL_LORA_GEMM, s, true);
-    void* args[] = {&ma, &mb, &p};
-    const cudaError_t e = cudaLaunchKernelExC(&cfg, fn, args);
-    timing_mark(QLORA_KERNEL_LORA_GEMM, s, false);
-    if (e != cudaSuccess) return QLORA_ERR_CUDA;
-    const qlora_status done = after_launch("rank_gemm", s);
-    if (done != QLORA_OK) return done;
-  }
-  return QLORA_OK;
+  count_launch();
+  timing_mark(QLORA_KERNEL_LORA_GEMM, s, true);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, ma, mb, p);
+  timing_mark(QLORA_KERNEL_LORA_GEMM, s, false);
+  if (e != cudaSuccess) return QLORA_ERR_CUDA;
+  return after_launch("rank_gemm", s);
 }
 
 }  // namespace qlora

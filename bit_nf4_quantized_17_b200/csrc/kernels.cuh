@@ -103,13 +103,12 @@ struct ReduceArgs;
 bool tc_rank_eligible(int32_t n_cols, int32_t cols, int32_t lo);
 int tc_rank_splits(int64_t m_tiles, int64_t k_tiles);
 // b_mn: B stored with its n_cols columns contiguous (element (j, k) at
-// k * ld_b + j, b_rows = n_cols); needs n_cols % 64 == 0.  short_chains (out.o1
-// alone): several accumulators, and launches that add where the contraction is long.
-// third: o3 gets a third bf16 term too, o3_lo rows behind the second (24 bits in all).
+// k * ld_b + j, b_rows = n_cols); needs n_cols % 64 == 0.  third: o3 gets a third bf16
+// term too, o3_lo rows behind the second (24 bits in all).
 qlora_status tc_rank_gemm(const void* A, bool a_mn, int64_t m_rows, int64_t kdim, int64_t ld_a,
                           const void* B, bool b_mn, int64_t ld_b, int32_t b_rows, int32_t n_cols,
                           const ReduceArgs& out, DeviceStatus* st, cudaStream_t s,
-                          bool short_chains = false, bool third = false);
+                          bool third = false);
 
 struct ReduceArgs {
   const float* part;

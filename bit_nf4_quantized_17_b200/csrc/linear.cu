@@ -398,7 +398,7 @@ qlora_status linear_backward(const qlora_nf4& W, const LevelTable& t, const void
       ra.a3 = 1.0f;
       ra.o3_lo = r16;
       if (v_direct) {
-        QLORA_TRY(tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s, false,
+        QLORA_TRY(tc_rank_gemm(dY, false, M, N, N, B, true, r, r, span, ra, st, s,
                                o.x8 != nullptr));
       } else if (o.x8) {
         return QLORA_ERR_UNSUPPORTED;  // V in three terms is the direct form's
