@@ -54,7 +54,7 @@ inline void choose_splits(const void* kernel, const cudaLaunchConfig_t& cfg, int
     const int64_t rounds = ceil_div(clusters, at_once(n, per, both));
     const int64_t cost =
         times * (rounds * (per * (both ? c.shared : 10) + c.start + c.split * n) + c.launch);
-    if (least != 0 && cost >= least) continue;
+    if (least != 0 && cost > least) continue;  // equal: fewer, which leave more to others
     least = cost;
     *splits = n;
     *launches = times;
