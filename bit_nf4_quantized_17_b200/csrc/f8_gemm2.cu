@@ -15,6 +15,9 @@
 // cores work on two accumulators while two are drained.  With one thread a row and
 // 128 columns a thread needs one scale of A and two of B per block.
 //
+// ptxas: 168 registers at launch, 40 bytes of stack (80 of spill stores, 160 of loads in the
+// code).  They come with the block of the LoRA term: without it there are none.
+//
 // Bound: 2048 x 8192 x 22016 takes 322 us in bursts (2.3 PFLOP/s), the same MMAs
 // without sums 250 us; sustained, the 1 kW power cap lowers the clock to 1.48 GHz
 // and it takes 384 us.  4096^3: 70 us.

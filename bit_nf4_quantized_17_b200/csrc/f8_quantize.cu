@@ -14,7 +14,12 @@
 // would saturate, into NaN.
 //
 // Both directions are bound by HBM: 2 bytes read and 1 written per value from
-// bf16 (the other way round when restoring), plus 4 bytes per block.
+// bf16 (the other way round when restoring), 4 and 1 from fp32, plus 4 bytes per block.
+// 8192 x 11008, warm launches over four matrices, floor 41.2 us from bf16 and 68.7 from fp32: by
+// rows 41.3 and 73.6, by tiles 42.3 and 89.5 (an fp32 tile is 64 registers a thread: two
+// CTAs an SM, whose load and store phases overlap less), restored 42.0 and 69.6, from tiles
+// 41.7 and 69.2.  (Four CTAs an SM cost the bf16 tiles of odd rows, 2-byte loads, 48 bytes of
+// spills; no other instance has any.)
 #include <cuda_fp8.h>
 
 #include "f8.cuh"

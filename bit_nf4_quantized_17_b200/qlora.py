@@ -523,7 +523,10 @@ def _f8_scales_shape(rows, cols, layout):
 
 class F8Matrix:
     """Caller-owned device arrays of a matrix held in 8 bits (see qlora_f8): codes (uint8,
-    rows x ld) and scales (fp32: blocks x rows, or row blocks x column blocks for tiles)."""
+    rows x ld) and scales (fp32: blocks x rows, or row blocks x column blocks for tiles).
+
+    pow2 is the caller's word that every scale is a power of two, at least 2^-126, and is not
+    checked: a product may then read the exponents only, and other scales give wrong sums."""
 
     __slots__ = ("rows", "cols", "layout", "format", "pow2", "codes", "scales", "struct")
 

@@ -303,8 +303,8 @@ qlora_status qlora_linear_bwd_ex(const qlora_nf4* W, const void* A, const void* 
  *           QLORA_F8_TILES: a scale per 128 x 128 tile, row-major:
  *           scales[(row / 128) * ceil(cols / 128) + col / 128] (weights)
  *   format  QLORA_E4M3 (largest value F = 448) or QLORA_E5M2 (F = 57344)
- *   pow2    1: every scale is a power of two (a product may then read its exponent
- *           only), 0: any fp32
+ *   pow2    1: every scale is a power of two, at least 2^-126 (not checked: a product may
+ *           then read its exponent only, and other scales give wrong sums), 0: any fp32
  *   codes   device, rows of ld bytes (ld a multiple of 16, at least cols)
  *   scales  device fp32
  * The value of an element is its code times its block's scale.  Sizes need not
@@ -349,7 +349,8 @@ qlora_status qlora_f8_dequantize(const qlora_f8* q, void* X_out, int32_t out_dty
  * C (device, m x n, row-major) is bf16 or fp32, rounded once from fp32 sums:
  *   C[i][j] = sum over 128-blocks b of k of
  *             sA[b][i] sB[b, j / 128] (sum over the block of codeA codeB).
- * The products sA sB have to be finite.  Needs no workspace; the tensor cores'
+ * The products sA sB have to be finite, and at least 2^-126 where the codes are not
+ * all zeros: they are formed in fp32 first, and bits below that are lost.  Needs no workspace; the tensor cores'
  * device-side waits are bounded, and as the call takes no status word, a wait that
  * gives up (it does not in correct operation) leaves NaN in its tile of C.
  * Errors: QLORA_ERR_NULL, _ALIGN, _SHAPE (contraction lengths differ, B without
@@ -363,7 +364,8 @@ qlora_status qlora_f8_matmul(const qlora_f8* A, const qlora_f8* B, int32_t trans
  * and takes the place of X in dA = s V^T X^, X^ = bf16(code * s) (what
  * qlora_f8_dequantize writes).  With dropout X8 is the kept form of the forward's x_drop,
  * and opts->x_drop is not read.  U (M x r fp32) from the forward is required.  dX and
- * dB do not depend on X.  opts may be NULL: one adapter, no dropout.  Workspace: at
+ * dB do not depend on X and are those of qlora_linear_bwd_ex, bit for bit.  dA reads all 24
+ * bits of V, whose sums over d_out are the NF4 layer's.  opts may be NULL: one adapter, no dropout.  Workspace: at
  * least the bytes of qlora_linear_bwd_f8_workspace (rank n_adapters r).  Errors as
  * qlora_linear_bwd_ex and qlora_f8_quantize. */
 qlora_status qlora_linear_bwd_f8_workspace(int64_t M, int64_t N, int64_t K, int32_t r,
@@ -383,7 +385,11 @@ qlora_status qlora_linear_bwd_f8(const qlora_nf4* W, const void* A, const void* 
  *   bwd  dY^ = 8 bits of dY (grad_format, layout QLORA_F8_ROWS, pow2 as X8), V = dY B,
  *        dX = dY^ W + s V A,  dB = s dY^T U,  dA = s V^T bf16(X^)
  * X, dY, Y, dX: bf16; A, B: bf16; U_save / U, dA, dB: fp32, as in the NF4 layer.  dX and
- * U_save may be NULL.  dA and dB are overwritten, or added to when accumulate != 0.
+ * U_save may be NULL.  dA and dB are overwritten, or added to when accumulate != 0.  U, dA and
+ * dB have fp32 precision: the rank-r products read all 24 bits of U and V, and the tensor
+ * cores' sums, which are cut off and not rounded, are kept short (about 1e-6 relative to
+ * exact sums at any number of tokens and up to 16384 columns; in Y and dX, which are bf16, s U
+ * and s V enter in 16 bits).
  * Requirements: r, d_out and d_in multiples of 8 (else QLORA_ERR_UNSUPPORTED),
  * 1 <= r <= 256, X8 of layout QLORA_F8_ROWS with d_in columns.  A workspace from
  * qlora_f8_linear_workspace, zero-filled before its first use, holds the status word. */
