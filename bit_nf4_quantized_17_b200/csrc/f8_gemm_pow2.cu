@@ -285,7 +285,8 @@ f8_pow2_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             ra[c][j] = scale_bits(p.sa + kb * p.m + min(row0 + 32 * c, p.m - 1));
 #pragma unroll
           for (int b = 0; b < 2; ++b)
-            rb[b][j] = scale_bits(p.sb + min(((nt * kBN) >> 7) + b, nbs - 1) * p.sb_n + kb * p.sb_k);
+            rb[b][j] =
+                scale_bits(p.sb + min(((nt * kBN) >> 7) + b, nbs - 1) * p.sb_n + kb * p.sb_k);
         }
         uint32_t wa[4], wb[8];
 #pragma unroll

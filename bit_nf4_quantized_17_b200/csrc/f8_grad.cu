@@ -18,15 +18,17 @@
 // and summed in distributed shared memory in split order, as in gemm_rank.cu.  V is fp32: it
 // enters as three bf16 terms (24 bits; two would leave dA off by 2.5e-6 relative).  Sums in
 // TMEM are cut off, not rounded, which adds up along a chain of MMAs: the first term's
-// products go tile by tile in turn into as many accumulators as keep its chains at 16 MMAs (256
-// tokens), as far as TMEM goes, the small products of the other two into one more, and
-// tokens past 48 MMAs a chain (64 above rank 64) are a launch of their own that adds to dA.  Relative to fp64 at
-// rank 16, 4096 columns: 4096 tokens 4.3e-7, 65536 8.8e-7 (2.7e-6 and 2.0e-5 with two terms in
-// one accumulator and launch).  Roles (384
-// threads): warp 0 loads codes, warp 2 loads V^T, warp 1 owns TMEM and issues
-// the MMAs, warps 4-11 expand in two groups (group g takes 64-token tiles
-// i % 2 == g) and drain.  Every wait is bounded; a wait that gives up
-// reports QLORA_ERR_DEVICE_TIMEOUT and leaves NaN in its columns of dA.
+// products go tile by tile in turn into as many accumulators as keep its chains at 16 MMAs
+// (256 tokens), as far as TMEM goes, the small products of the other two into one more, and
+// tokens past 48 MMAs a chain (64 above rank 64) are a launch of their own that adds to dA.
+// Relative to fp64 at rank 16, 4096 columns: 4096 tokens 4.3e-7, 65536 8.8e-7 (2.7e-6 and
+// 2.0e-5 with two terms in one accumulator and launch).
+//
+// Roles (384 threads): warp 0 loads codes, warp 2 loads V^T, warp 1 owns TMEM and issues the
+// MMAs, warps 4-11 expand in two groups (group g takes 64-token tiles i % 2 == g) and drain.
+// Every wait is bounded; a wait that gives up reports QLORA_ERR_DEVICE_TIMEOUT and leaves NaN
+// in its columns of dA.
+//
 // Up to 16 tokens: CUDA cores, bound by writing dA; a thread takes 16 columns of 4
 // ranks, so that each code is expanded once for 4 ranks.
 #include <cudaTypedefs.h>
@@ -431,7 +433,8 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
     return kAlignSlack + p.area + barrier_bytes(stages);
   };
   const bool two = need(kStages) <= kCtaHalfSmem;
-  for (p.v_stages = kMaxVStages; need(p.v_stages) > (two ? kCtaHalfSmem : kCtaMaxSmem);) --p.v_stages;
+  p.v_stages = kMaxVStages;
+  while (need(p.v_stages) > (two ? kCtaHalfSmem : kCtaMaxSmem)) --p.v_stages;
   const int smem = need(p.v_stages);
   int max_accs = 1;
   while ((2 * max_accs + 1) * p.rc <= (two ? 256 : 512)) max_accs *= 2;
@@ -456,7 +459,7 @@ qlora_status f8_grad_a(const void* vt, int64_t ld_v, const qlora_f8& x, int32_t 
     cfg.gridDim = dim3(static_cast<unsigned>(tiles), chunks, n);
   };
   // Splits of the tokens, at least 4 tiles each: whichever ends soonest.  In tenths of a tile's
-  // time a launch takes 60 and, a round of clusters that run at once, 10 a tile (18 where two
+  // time a launch takes 60 and, a round of clusters that run at once, 10 a tile (17 where two
   // CTAs share an SM), 40 for the start and 6 a split for the sum.  Backward without dX, d_in
   // 4096, rank 16, in 4 and in 8 splits: 4096 tokens 34.4 and 33.7 us, 8192 57.3 and 52.7;
   // 2048 at rank 64 34.1 and 34.6; d_in 2048, rank 128, 4096 tokens, in 6 and 8 (two

@@ -268,8 +268,8 @@ qlora_status f8_grad_b(const void* dY, int64_t N, const float* U, int64_t M, int
                        cudaStream_t s) {
   const int32_t r16 = lora_rows(r);
   count_launch();
-  terms_kernel<<<dim3(static_cast<unsigned>(ceil_div(M, 64)), static_cast<unsigned>(ceil_div(r, 32))),
-                 256, 0, s>>>(U, M, r, static_cast<__nv_bfloat16*>(ut), ld_u, ld_u * r16);
+  const dim3 grid(static_cast<unsigned>(ceil_div(M, 64)), static_cast<unsigned>(ceil_div(r, 32)));
+  terms_kernel<<<grid, 256, 0, s>>>(U, M, r, static_cast<__nv_bfloat16*>(ut), ld_u, ld_u * r16);
   QLORA_TRY(after_launch("f8_grad_b terms", s));
   GradBArgs p{};
   const int chunks = r16 > 128 ? 2 : 1;
@@ -291,7 +291,8 @@ qlora_status f8_grad_b(const void* dY, int64_t N, const float* U, int64_t M, int
   // two CTAs an SM where two stages fit beside another's, else one; as many stages as do
   const int stage_bytes = kABytes + kTerms * p.rc * 128;
   const bool two = 2 * stage_bytes + kBesideBytes <= kCtaHalfSmem;
-  p.stages = std::min(kMaxStages, ((two ? kCtaHalfSmem : kCtaMaxSmem) - kBesideBytes) / stage_bytes);
+  p.stages =
+      std::min(kMaxStages, ((two ? kCtaHalfSmem : kCtaMaxSmem) - kBesideBytes) / stage_bytes);
   p.area = std::max(p.stages * stage_bytes, 128 * (p.rc + 4) * 4);
   int max_accs = 1;
   while ((2 * max_accs + 1) * p.rc <= (two ? 256 : 512)) max_accs *= 2;

@@ -41,7 +41,7 @@ def test_pair_ring_reads_stay_in_their_chunk(tmp_path):
     src.write_text(PROGRAM)
     csrc = os.path.join(ROOT, "bit_nf4_quantized_17_b200", "csrc")
     subprocess.run([cxx, "-std=c++17", "-I", csrc, "-o", str(exe), str(src)], check=True)
-    lines = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split("\n")
-    rows = [tuple(map(int, x.split())) for x in lines if x]
+    out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
+    rows = [tuple(map(int, x.split())) for x in out.splitlines()]
     assert len(rows) == 4 * 17
     assert [r for r in rows if not r[2]] == []

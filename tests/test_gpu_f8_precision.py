@@ -55,8 +55,8 @@ def test_factor_over_many_columns(M, K, r):
     assert _off(U, X.double() @ A.double().t()) < 3e-6
 
 
-SHORT = [(2048, 256, 4096, 16), (1000, 64, 1024, 64), (1024, 200, 1024, 128), (300, 256, 2048, 24),
-         (17, 256, 704, 256)]
+SHORT = [(2048, 256, 4096, 16), (1000, 64, 1024, 64), (1024, 200, 1024, 128),
+         (300, 256, 2048, 24), (17, 256, 704, 256)]
 
 
 @pytest.mark.parametrize("M,N,K,r", SHORT)
@@ -72,7 +72,8 @@ def test_grad_a_reads_all_of_v(M, N, K, r):
     assert _off(dA, want) < 1.2e-6
 
 
-LONG = [(16384, 256, 4096, 16), (16384, 22016, 256, 64), (8192, 128, 11008, 32), (20001, 72, 2048, 128),
+LONG = [(16384, 256, 4096, 16), (16384, 22016, 256, 64), (8192, 128, 11008, 32),
+        (20001, 72, 2048, 128),
         (65536, 136, 1032, 64), (9000, 64, 11008, 256), (33000, 64, 200, 160)]
 
 
@@ -113,7 +114,8 @@ def test_grad_b_over_many_tokens(M, N, K, r):
     assert _off(dB2, 2 * want) < 3e-6
 
 
-@pytest.mark.parametrize("M,N,K,r", [(2048, 4096, 64, 16), (1000, 1032, 64, 64), (512, 200, 64, 128),
+@pytest.mark.parametrize("M,N,K,r", [(2048, 4096, 64, 16), (1000, 1032, 64, 64),
+                                     (512, 200, 64, 128),
                                      (500, 256, 64, 24), (17, 264, 64, 256), (130, 8, 64, 72)])
 def test_grad_b_reads_all_of_u(M, N, K, r):
     W, A, B, X, dY = _inputs(M, N, K, r)
